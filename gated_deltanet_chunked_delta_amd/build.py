@@ -14,9 +14,12 @@ LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(PKG, "csrc", "gdn_fused.hip"), os.path.join(PKG, "csrc", "gdn_fused_ws.hip"),
            os.path.join(PKG, "csrc", "gdn_recurrent.hip"), os.path.join(PKG, "csrc", "gdn_gating.hip"),
            os.path.join(PKG, "csrc", "gdn_split.hip"), os.path.join(PKG, "csrc", "gdn_backward.hip"),
+           os.path.join(PKG, "csrc", "gdn_steps.hip"), os.path.join(PKG, "csrc", "gdn_conv.hip"),
+           os.path.join(PKG, "csrc", "gdn_norm.hip"),
            os.path.join(PKG, "csrc", "gdn_api.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "gdn.h"), os.path.join(PKG, "csrc", "gdn_internal.h"),
-           os.path.join(PKG, "csrc", "gdn_device.h")]
+           os.path.join(PKG, "csrc", "gdn_device.h"), os.path.join(PKG, "csrc", "gdn_layer.h"),
+           os.path.join(PKG, "csrc", "gdn_layer_device.h")]
 
 # Packed fp32 VALU instructions are kept out of the generated code.  MFMA
 # accumulators are kept in VGPRs: the kernels consume every accumulator with

@@ -12,6 +12,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_layer.h"
 
 namespace gdn {
 // Gate-input gradients (gdn_gating.hip).
@@ -65,9 +66,9 @@ struct EventProfiler : gdn::Profiler {
     std::atomic<bool> on{false};
     std::vector<hipEvent_t> pool;
     std::vector<Rec> pending;
-    hipEvent_t open[gdn::kNumKernelKinds] = {};
-    double total_ms[gdn::kNumKernelKinds] = {};
-    int64_t launches[gdn::kNumKernelKinds] = {};
+    hipEvent_t open[gdn::kNumAllKinds] = {};
+    double total_ms[gdn::kNumAllKinds] = {};
+    int64_t launches[gdn::kNumAllKinds] = {};
 
     hipEvent_t take() {
         if (!pool.empty()) {
@@ -106,7 +107,7 @@ struct EventProfiler : gdn::Profiler {
     }
     void reset() {
         drain();
-        for (int i = 0; i < gdn::kNumKernelKinds; ++i) {
+        for (int i = 0; i < gdn::kNumAllKinds; ++i) {
             total_ms[i] = 0.0;
             launches[i] = 0;
         }
@@ -328,6 +329,149 @@ int chunk_bwd(const void *q, const void *k, const void *v, const float *g, const
     return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
+// ---------------------------------------------------------------------------
+// The operators around the delta rule.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads: 2^32 threads a launch
+
+// Slots of a few-token step: data and indices given, a known dtype, at least one
+// slot and one column, data aligned to `align` bytes.
+int check_slots(const gdn_step_pool &pl, uintptr_t align) {
+    if (!pl.data || !pl.indices) return GDN_ERR_NULL;
+    if (pl.pool_size < 1 || pl.cols < 1) return GDN_ERR_SHAPE;
+    if (((uintptr_t)pl.data & (align - 1)) != 0) return GDN_ERR_ALIGN;
+    if ((((uintptr_t)pl.indices | (uintptr_t)pl.num_accepted) & 3u) != 0) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+gdn::StepSlots slots_of(const gdn_step_pool &pl) {
+    return gdn::StepSlots{pl.data, pl.indices, pl.num_accepted, pl.pool_size, pl.cols};
+}
+
+// Sizes of a convolution and the pieces of its output (or its gradient).
+int check_conv(const gdn_conv_shape *shape, const gdn_conv_pieces *pieces, const int32_t *cu_seqlens) {
+    if (!shape) return GDN_ERR_NULL;
+    const gdn_conv_shape &s = *shape;
+    if (s.B < 0 || s.T < 0 || s.N < 0 || s.D <= 0) return GDN_ERR_SHAPE;
+    if (gdn::elem_bytes(s.dtype) == 0 || gdn::elem_bytes(s.weight_dtype) == 0) return GDN_ERR_DTYPE;
+    if (s.W < 2 || s.W > 4) return GDN_ERR_UNSUPPORTED;
+    if (s.weight_dtype != s.dtype && s.weight_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+    if (cu_seqlens ? s.B != 1 : s.N != s.B) return GDN_ERR_SHAPE;
+    const int64_t tokens = (int64_t)s.B * s.T;
+    if (tokens > INT_MAX - 64 || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
+    if (tokens > 0 && s.x_stride < s.D) return GDN_ERR_SHAPE;
+    if (s.x_stride > ((int64_t)1 << 31) || gdn::conv_grid(tokens, s.D, s.N) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (((uintptr_t)cu_seqlens & 3u) != 0) return GDN_ERR_ALIGN;
+    if (!pieces) return GDN_ERR_NULL;
+    int64_t sum = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (pieces->dim[i] < 0) return GDN_ERR_SHAPE;
+        sum += pieces->dim[i];
+        if (tokens > 0 && pieces->dim[i] > 0 && !pieces->ptr[i]) return GDN_ERR_NULL;
+        if (((uintptr_t)pieces->ptr[i] & (uintptr_t)(gdn::elem_bytes(s.dtype) - 1)) != 0) return GDN_ERR_ALIGN;
+    }
+    return sum == s.D ? GDN_OK : GDN_ERR_SHAPE;
+}
+
+int check_conv_inputs(const gdn_conv_shape &s, const void *x, const void *weight, const void *bias,
+                      const void *state_a, const void *state_b) {
+    if (!weight || ((int64_t)s.B * s.T > 0 && !x)) return GDN_ERR_NULL;
+    const uintptr_t e = (uintptr_t)gdn::elem_bytes(s.dtype) - 1, we = (uintptr_t)gdn::elem_bytes(s.weight_dtype) - 1;
+    if ((((uintptr_t)x | (uintptr_t)state_a | (uintptr_t)state_b) & e) != 0) return GDN_ERR_ALIGN;
+    if ((((uintptr_t)weight | (uintptr_t)bias) & we) != 0) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+gdn::ConvParams conv_params(const gdn_conv_shape &s, const gdn_conv_pieces &pieces, const void *x, const void *weight,
+                            const void *bias, int silu, const int32_t *cu_seqlens) {
+    gdn::ConvParams p{};
+    p.x = x;
+    p.x_stride = s.x_stride;
+    p.weight = weight;
+    p.bias = bias;
+    p.w_f32 = s.weight_dtype == GDN_F32;
+    p.silu = silu ? 1 : 0;
+    p.cu_seqlens = cu_seqlens;
+    for (int i = 0; i < 3; ++i) {
+        p.piece[i] = pieces.ptr[i];
+        p.piece_dim[i] = pieces.dim[i];
+    }
+    p.T = s.T;
+    p.T_tot = s.B * s.T;
+    p.D = s.D;
+    p.W = s.W;
+    p.N = s.N;
+    return p;
+}
+
+int conv_fwd(const void *x, const void *weight, const void *bias, int silu, const void *initial_state,
+             const gdn_state_pool *pool, const int32_t *cu_seqlens, const gdn_conv_pieces *out, void *final_state,
+             const gdn_conv_shape *shape, void *stream) {
+    int st = check_conv(shape, out, cu_seqlens);
+    if (st != GDN_OK) return st;
+    st = check_conv_inputs(*shape, x, weight, bias, initial_state, final_state);
+    if (st != GDN_OK) return st;
+    gdn::ConvParams p = conv_params(*shape, *out, x, weight, bias, silu, cu_seqlens);
+    p.initial = initial_state;
+    p.final_state = final_state;
+    if (pool && shape->N > 0) {
+        if (!pool->data || !pool->indices) return GDN_ERR_NULL;
+        if (pool->dtype != shape->dtype) return GDN_ERR_DTYPE;
+        if (pool->pool_size < 1) return GDN_ERR_SHAPE;
+        if (((uintptr_t)pool->data & (uintptr_t)(gdn::elem_bytes(shape->dtype) - 1)) != 0 ||
+            ((uintptr_t)pool->indices & 3u) != 0)
+            return GDN_ERR_ALIGN;
+        p.initial = pool->read_initial ? pool->data : nullptr;
+        p.final_state = pool->data;
+        p.indices = pool->indices;
+        p.pool_size = pool->pool_size;
+    }
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_conv(p, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// Sizes of a norm over rows of at most max_d elements.
+int check_norm(const gdn_norm_shape *shape, int max_d, const void *weight) {
+    if (!shape) return GDN_ERR_NULL;
+    const gdn_norm_shape &s = *shape;
+    if (s.rows < 0 || s.rows > INT_MAX || s.D <= 0) return GDN_ERR_SHAPE;
+    if (gdn::elem_bytes(s.dtype) == 0 || gdn::elem_bytes(s.weight_dtype) == 0) return GDN_ERR_DTYPE;
+    if (s.D > max_d || (s.weight_dtype != s.dtype && s.weight_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
+    if (!weight) return GDN_ERR_NULL;
+    if (((uintptr_t)weight & (uintptr_t)(gdn::elem_bytes(s.weight_dtype) - 1)) != 0) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+int check_gated(const gdn_norm_shape *shape, const void *weight) {
+    const int st = check_norm(shape, gdn::kGatedMaxD, weight);
+    if (st != GDN_OK) return st;
+    // z: tokens of heads rows each, z_stride elements apart
+    if (shape->heads <= 0 || shape->rows % shape->heads != 0) return GDN_ERR_SHAPE;
+    if (shape->z_stride < (int64_t)shape->heads * shape->D || shape->z_stride > ((int64_t)1 << 31)) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+gdn::NormParams norm_params(const gdn_norm_shape &s, const void *weight, float eps) {
+    gdn::NormParams p{};
+    p.weight = weight;
+    p.rows = s.rows;
+    p.D = s.D;
+    p.heads = s.heads;
+    p.z_stride = s.z_stride;
+    p.eps = eps;
+    p.w_f32 = s.weight_dtype == GDN_F32;
+    return p;
+}
+template <class... P> bool misaligned(int dtype, P... ptr) {
+    return (((uintptr_t)0 | ... | (uintptr_t)ptr) & (uintptr_t)(gdn::elem_bytes(dtype) - 1)) != 0;
+}
+int check_norm_ws(const gdn_norm_shape &s, const float *dweight, const void *workspace, size_t workspace_bytes) {
+    if (!dweight) return GDN_ERR_NULL;
+    if (((uintptr_t)dweight & 3u) != 0) return GDN_ERR_ALIGN;
+    const size_t need = gdn::norm_bwd_workspace_bytes(s.rows, s.D);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GDN_ERR_WORKSPACE;
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -356,13 +500,13 @@ int gdn_profile_enable(int enable) {
 int gdn_profile_read(int max_kinds, const char **names, double *total_ms, int64_t *launches) {
     std::lock_guard<std::mutex> lock(g_prof.mu);
     g_prof.drain();
-    const int n = max_kinds < gdn::kNumKernelKinds ? max_kinds : gdn::kNumKernelKinds;
+    const int n = max_kinds < gdn::kNumAllKinds ? max_kinds : gdn::kNumAllKinds;
     for (int i = 0; i < n; ++i) {
-        if (names) names[i] = gdn::kernel_name(i);
+        if (names) names[i] = i < gdn::kNumKernelKinds ? gdn::kernel_name(i) : gdn::layer_kernel_name(i);
         if (total_ms) total_ms[i] = g_prof.total_ms[i];
         if (launches) launches[i] = g_prof.launches[i];
     }
-    return gdn::kNumKernelKinds;
+    return gdn::kNumAllKinds;
 }
 
 size_t gdn_chunk_fwd_workspace_bytes(const gdn_shape *shape) {
@@ -480,6 +624,201 @@ int gdn_gating_bwd(const gdn_gates *gates, int64_t rows, int32_t HV, int32_t dty
     const gdn::Gates gt{gates->A_log, gates->dt_bias, gates->a, gates->b};
     const hipError_t err = gdn::launch_gating_bwd(gt, rows, HV, dtype, dg, dbeta, da, db, dA_log, ddt_bias,
                                                   (float *)workspace, (hipStream_t)stream);
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_recurrent_steps(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                        const gdn_gates *gates, float scale, int use_l2norm, const gdn_step_pool *pool,
+                        const int32_t *cu_seqlens, void *out, const gdn_shape *shape, void *stream) {
+    const int st = check_shape(shape);
+    if (st != GDN_OK) return st;
+    const gdn_shape &s = *shape;
+    if (cu_seqlens ? s.B != 1 : s.N != s.B) return GDN_ERR_SHAPE;
+    const int64_t tokens = (int64_t)s.B * s.T;
+    if ((s.N == 0 && tokens > 0) || (int64_t)s.N * s.HV > kMaxGrid) return GDN_ERR_SHAPE;
+    if (((uintptr_t)cu_seqlens & 3u) != 0) return GDN_ERR_ALIGN;
+    if (!pool) return GDN_ERR_NULL;
+    if (pool->dtype != GDN_BF16 && pool->dtype != GDN_F32) return GDN_ERR_DTYPE;
+    if (tokens == 0) return GDN_OK;
+    if (!q || !k || !v || !out || (!gates && (!g || !beta))) return GDN_ERR_NULL;
+    if (misaligned(s.dtype, q, k, v, out) || (((uintptr_t)g | (uintptr_t)beta) & 3u) != 0) return GDN_ERR_ALIGN;
+    if (gates) {
+        const int gs = check_gates(*gates);
+        if (gs != GDN_OK) return gs;
+    }
+    const int ps = check_slots(*pool, pool->dtype == GDN_BF16 ? 8 : 16);
+    if (ps != GDN_OK) return ps;
+    gdn::StepsParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    if (gates) p.gates = gdn::Gates{gates->A_log, gates->dt_bias, gates->a, gates->b};
+    p.slots = slots_of(*pool);
+    p.state_bf16 = pool->dtype == GDN_BF16;
+    p.cu_seqlens = cu_seqlens;
+    p.out = out;
+    p.T = s.T;
+    p.T_tot = (int)tokens;
+    p.H = s.H;
+    p.HV = s.HV;
+    p.K = s.K;
+    p.V = s.V;
+    p.N = s.N;
+    p.scale = scale;
+    p.use_l2norm = use_l2norm ? 1 : 0;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_steps(p, s.dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_conv_fwd(const void *x, const void *weight, const void *bias, int silu, const void *initial_state,
+                 const int32_t *cu_seqlens, const gdn_conv_pieces *out, void *final_state,
+                 const gdn_conv_shape *shape, void *stream) {
+    return conv_fwd(x, weight, bias, silu, initial_state, nullptr, cu_seqlens, out, final_state, shape, stream);
+}
+
+int gdn_conv_fwd_pool(const void *x, const void *weight, const void *bias, int silu, const gdn_state_pool *pool,
+                      const int32_t *cu_seqlens, const gdn_conv_pieces *out, const gdn_conv_shape *shape,
+                      void *stream) {
+    if (!pool) return GDN_ERR_NULL;
+    return conv_fwd(x, weight, bias, silu, nullptr, pool, cu_seqlens, out, nullptr, shape, stream);
+}
+
+int gdn_conv_update(const void *x, const void *weight, const void *bias, int silu, const gdn_step_pool *pool,
+                    const int32_t *cu_seqlens, const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream) {
+    int st = check_conv(shape, out, cu_seqlens);
+    if (st != GDN_OK) return st;
+    if (!pool) return GDN_ERR_NULL;
+    if (pool->dtype != shape->dtype) return GDN_ERR_DTYPE;
+    if ((int64_t)shape->B * shape->T == 0) return GDN_OK;
+    st = check_conv_inputs(*shape, x, weight, bias, nullptr, nullptr);
+    if (st != GDN_OK) return st;
+    st = check_slots(*pool, gdn::elem_bytes(shape->dtype));
+    if (st != GDN_OK) return st;
+    gdn::ConvParams p = conv_params(*shape, *out, x, weight, bias, silu, cu_seqlens);
+    p.slots = slots_of(*pool);
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_conv_update(p, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape) {
+    if (!shape || shape->B < 0 || shape->T < 0 || shape->D <= 0 || shape->W < 2 || shape->W > 4) return 0;
+    const int64_t tokens = (int64_t)shape->B * shape->T;
+    return tokens > INT_MAX - 64 ? 0 : gdn::conv_bwd_workspace_bytes(tokens, shape->D, shape->W);
+}
+
+int gdn_conv_bwd(const void *x, const void *weight, const void *bias, int silu, const void *initial_state,
+                 const int32_t *cu_seqlens, const gdn_conv_pieces *dout, void *dx, float *dweight, float *dbias,
+                 void *dinitial, const gdn_conv_shape *shape, void *workspace, size_t workspace_bytes,
+                 void *stream) {
+    int st = check_conv(shape, dout, cu_seqlens);
+    if (st != GDN_OK) return st;
+    st = check_conv_inputs(*shape, x, weight, bias, initial_state, dinitial);
+    if (st != GDN_OK) return st;
+    const gdn_conv_shape &s = *shape;
+    const int64_t tokens = (int64_t)s.B * s.T;
+    if (!dweight || (tokens > 0 && !dx)) return GDN_ERR_NULL;
+    if (misaligned(s.dtype, dx) || (((uintptr_t)dweight | (uintptr_t)dbias) & 3u) != 0) return GDN_ERR_ALIGN;
+    const size_t need = gdn::conv_bwd_workspace_bytes(tokens, s.D, s.W);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GDN_ERR_WORKSPACE;
+    gdn::ConvParams p = conv_params(s, *dout, x, weight, bias, silu, cu_seqlens);
+    p.initial = initial_state;
+    p.dx = dx;
+    p.dweight = dweight;
+    p.dbias = dbias;
+    p.dinitial = dinitial;
+    p.part = (float *)workspace;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_conv_bwd(p, s.dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_gated_norm(const void *x, const void *z, const void *weight, float eps, void *out,
+                   const gdn_norm_shape *shape, void *stream) {
+    const int st = check_gated(shape, weight);
+    if (st != GDN_OK) return st;
+    if (shape->rows == 0) return GDN_OK;
+    if (!x || !z || !out) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, x, z, out)) return GDN_ERR_ALIGN;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.x = x;
+    p.z = z;
+    p.y = out;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_norm(p, true, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_add_norm(const void *x, const void *residual, const void *weight, float residual_scale, float weight_offset,
+                 float eps, void *out, void *hidden, const gdn_norm_shape *shape, void *stream) {
+    const int st = check_norm(shape, gdn::kNormMaxD, weight);
+    if (st != GDN_OK) return st;
+    if (shape->rows == 0) return GDN_OK;
+    if (!x || !out) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, x, residual, out, hidden)) return GDN_ERR_ALIGN;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.x = x;
+    p.residual = residual;
+    p.y = out;
+    p.hidden = hidden;
+    p.alpha = residual_scale;
+    p.offset = weight_offset;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_norm(p, false, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape *shape) {
+    if (!shape || shape->rows < 0 || shape->rows > INT_MAX || shape->D <= 0 || shape->D > gdn::kNormMaxD) return 0;
+    return gdn::norm_bwd_workspace_bytes(shape->rows, shape->D);
+}
+
+int gdn_gated_norm_bwd(const void *x, const void *z, const void *weight, float eps, const void *dout, void *dx,
+                       void *dz, float *dweight, const gdn_norm_shape *shape, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    int st = check_gated(shape, weight);
+    if (st != GDN_OK) return st;
+    if (shape->rows > 0 && (!x || !z || !dout || !dx || !dz)) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, x, z, dout, dx, dz)) return GDN_ERR_ALIGN;
+    st = check_norm_ws(*shape, dweight, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.x = x;
+    p.z = z;
+    p.dy = dout;
+    p.dx = dx;
+    p.dz = dz;
+    p.dweight = dweight;
+    p.part = (float *)workspace;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_norm_bwd(p, true, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, const void *weight,
+                     float residual_scale, float weight_offset, float eps, void *dx, void *dresidual, float *dweight,
+                     const gdn_norm_shape *shape, void *workspace, size_t workspace_bytes, void *stream) {
+    int st = check_norm(shape, gdn::kNormMaxD, weight);
+    if (st != GDN_OK) return st;
+    if (shape->rows > 0 && (!dout || !hidden || (!dx && !dresidual))) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, dout, dhidden, hidden, dx, dresidual)) return GDN_ERR_ALIGN;
+    st = check_norm_ws(*shape, dweight, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.hidden = const_cast<void *>(hidden);
+    p.dy = dout;
+    p.dhidden = dhidden;
+    p.dx = dx;
+    p.dresidual = dresidual;
+    p.dweight = dweight;
+    p.alpha = residual_scale;
+    p.offset = weight_offset;
+    p.part = (float *)workspace;
+    const hipError_t err = with_profiler(
+        [&](gdn::Profiler *prof) { return gdn::launch_norm_bwd(p, false, shape->dtype, (hipStream_t)stream, prof); });
     return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

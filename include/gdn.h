@@ -411,6 +411,222 @@ int gdn_chunk_bwd(const void *q, const void *k, const void *v,
                   const gdn_shape *shape, void *workspace, size_t workspace_bytes,
                   void *stream);
 
+/* Slots of a pool that a step of a few tokens per sequence reads and writes: a
+ * token and its drafts, verified in one call.  The states (gdn_recurrent_steps)
+ * or convolution histories (gdn_conv_update) of the running sequences lie in
+ * `pool_size` slots; sequence n has `cols` of them, indices[n, 0 .. cols-1].
+ *
+ *   data          the slots (device): [pool_size, HV, K, V] or [pool_size, D, W-1]
+ *                 of dtype; states are 16-byte aligned in fp32 and 8-byte in
+ *                 bf16, histories to their element (GDN_ERR_ALIGN otherwise)
+ *   indices       [N, cols] int32 (device)
+ *   num_accepted  [N] int32 (device) or NULL: how many tokens of the sequence's
+ *                 step before were kept, a.  The sequence starts from slot
+ *                 indices[n, a - 1], a taken into [1, cols]; NULL means a = 1
+ *   pool_size, cols  at least 1
+ *   dtype         gdn_dtype of the slots
+ *
+ * After the call slot indices[n, c], c < cols - 1, holds the state after the
+ * sequence's token c + 1, and slot indices[n, cols - 1] the state after its last
+ * token (where the sequence has cols tokens or more); the slots of columns that
+ * the sequence does not reach are left as they were.  With cols = 1 that is the
+ * in-place update of one slot per sequence, for any number of tokens.  A start
+ * slot outside [0, pool_size) (the sentinel -1 included) marks a padding row:
+ * its rows of out are zeros and nothing is stored.  A slot to be written that
+ * lies outside the pool is skipped.  The start state is read before any slot of
+ * the row is written, and a slot named twice in a row ends with the later
+ * token's state; two sequences must not name the same slot. */
+typedef struct gdn_step_pool {
+    void *data;
+    const int32_t *indices;
+    const int32_t *num_accepted;
+    int32_t pool_size, cols;
+    int32_t dtype;
+} gdn_step_pool;
+
+/* The recurrence over a few tokens per sequence, states in a pool (the
+ * multi-token decode of the LightLLM page "gdn.py", which verifies a token's
+ * drafts from the state behind the last accepted one).  Each token is applied
+ * as in gdn_recurrent_update, in order; the work of a sequence is serial in its
+ * tokens, so long prompts belong to gdn_chunk_fwd_pool.
+ *
+ *   q, k, v, out  [B, T, ...] as for gdn_chunk_fwd (with cu_seqlens B = 1 and
+ *                 sequences of any lengths, 0 included); aligned to their element
+ *   g, beta       [B, T, HV] fp32, or NULL with `gates` (rows = B * T)
+ *   pool          see gdn_step_pool
+ *   shape         as for gdn_chunk_fwd; at most 2^24 - 1 (sequence, value head) pairs
+ *
+ * No workspace.  out must not overlap any input or the pool.  Returns GDN_OK,
+ * GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN
+ * or GDN_ERR_LAUNCH; a call without tokens does nothing. */
+int gdn_recurrent_steps(const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, const gdn_gates *gates,
+                        float scale, int use_l2norm,
+                        const gdn_step_pool *pool, const int32_t *cu_seqlens, void *out,
+                        const gdn_shape *shape, void *stream);
+
+/* Sizes of the short convolution.
+ *   B, T, N       as in gdn_shape (with cu_seqlens B = 1)
+ *   D, W          columns, and the width: 2, 3 or 4 (GDN_ERR_UNSUPPORTED)
+ *   dtype         gdn_dtype of x, the outputs and the histories
+ *   weight_dtype  of weight and bias: dtype or GDN_F32
+ *   x_stride      elements between the rows of x, at least D (x may be a part
+ *                 of a wider projection's rows) and at most 2^31 */
+typedef struct gdn_conv_shape {
+    int32_t B, T, D, W, N;
+    int32_t dtype, weight_dtype;
+    int64_t x_stride;
+} gdn_conv_shape;
+
+/* The D columns of the convolution's output (or of its gradient) as up to three
+ * contiguous tensors [B, T, dim[i]], in order: q, k and v for the delta rule,
+ * without a copy that parts them.  The dims sum to D; a dim of 0 has no tensor. */
+typedef struct gdn_conv_pieces {
+    void *ptr[3];
+    int32_t dim[3];
+} gdn_conv_pieces;
+
+/* Causal depthwise convolution over the last W tokens, with SiLU: the operator
+ * in front of the delta rule (causal_conv1d_fn of the FastDeploy PR #7024 page,
+ * "Usage or Command", and of the LightLLM page's prefill).
+ *
+ *   pre[t, d] = bias[d] + sum_j weight[d, j] x[t - (W-1) + j, d]
+ *   out[t, d] = pre / (1 + e^-pre)   (silu != 0), or pre
+ *
+ * where the rows before a sequence's first are its start history.
+ *
+ *   x             [B, T, D]       dtype          read, rows x_stride apart
+ *   weight, bias  [D, W], [D]     weight_dtype   read; bias may be NULL
+ *   initial_state [N, D, W-1]     dtype or NULL  read: the W-1 inputs before the
+ *                 first token, oldest first; NULL = zeros
+ *   cu_seqlens    as for gdn_chunk_fwd
+ *   out           see gdn_conv_pieces            written (every element)
+ *   final_state   [N, D, W-1]     dtype or NULL  written: the last W-1 inputs
+ *                 (an empty sequence's is its initial state); may alias
+ *                 initial_state exactly, must not overlap anything else
+ *
+ * Tensors are aligned to their element.  Arithmetic is fp32, rounded once.  No
+ * workspace.  Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a
+ * sequence, more than 2^31 - 65 of them, or too many for one launch: 2^24 - 1
+ * blocks of 128 tokens by 512 columns), GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED,
+ * GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
+int gdn_conv_fwd(const void *x, const void *weight, const void *bias, int silu,
+                 const void *initial_state, const int32_t *cu_seqlens,
+                 const gdn_conv_pieces *out, void *final_state,
+                 const gdn_conv_shape *shape, void *stream);
+
+/* gdn_conv_fwd with the histories in a pool [pool_size, D, W-1] of dtype, in
+ * place, as gdn_chunk_fwd_pool has the states: a slot outside the pool gives a
+ * sequence zeros before it and stores nothing; read_initial = 0 starts all of
+ * them from zeros. */
+int gdn_conv_fwd_pool(const void *x, const void *weight, const void *bias, int silu,
+                      const gdn_state_pool *pool, const int32_t *cu_seqlens,
+                      const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream);
+
+/* The convolution of a few tokens per sequence with the histories in a pool
+ * (causal_conv1d_update of the same pages), next to gdn_recurrent_update and
+ * gdn_recurrent_steps: see gdn_step_pool, whose dtype is the shape's.  A
+ * sequence's tokens are taken in order by one wave. */
+int gdn_conv_update(const void *x, const void *weight, const void *bias, int silu,
+                    const gdn_step_pool *pool, const int32_t *cu_seqlens,
+                    const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream);
+
+/* Bytes of device workspace gdn_conv_bwd needs: W + 1 floats per column for
+ * each block of 32 to 256 tokens; 0 for invalid sizes or without tokens. */
+size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape);
+
+/* Backward pass of gdn_conv_fwd (training).  With dpre = dout silu'(pre),
+ *
+ *   dx[t]      = sum_j weight[j] dpre[t + (W-1) - j]     (inside the sequence)
+ *   dweight[j] = sum_t dpre[t] x[t - (W-1) + j],  dbias = sum_t dpre[t]
+ *
+ *   x, weight, bias, silu, initial_state, cu_seqlens, shape  as in the forward call
+ *   dout          see gdn_conv_pieces            read
+ *   dx            [B, T, D] contiguous, dtype    written (every element)
+ *   dweight       [D, W] fp32                    written
+ *   dbias         [D] fp32 or NULL               written
+ *   dinitial      [N, D, W-1] dtype or NULL      written: gradient of initial_state
+ *   workspace     gdn_conv_bwd_workspace_bytes bytes, 16-byte aligned
+ *                 (GDN_ERR_WORKSPACE); contents on entry are ignored
+ *
+ * The sums over tokens are taken in a fixed order.  Outputs must not overlap
+ * each other, the inputs or the workspace. */
+int gdn_conv_bwd(const void *x, const void *weight, const void *bias, int silu,
+                 const void *initial_state, const int32_t *cu_seqlens,
+                 const gdn_conv_pieces *dout, void *dx, float *dweight, float *dbias, void *dinitial,
+                 const gdn_conv_shape *shape, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Sizes of a norm.
+ *   rows          rows (tokens, or tokens times heads), at most 2^31 - 1
+ *   D             elements of a row: at most 1024 for the gated norm and 16384
+ *                 for the other (GDN_ERR_UNSUPPORTED)
+ *   dtype, weight_dtype  as in gdn_conv_shape
+ *   heads, z_stride  gated norm only: z is [rows / heads, heads, D] with z_stride
+ *                 elements between its tokens (>= heads * D, at most 2^31), so
+ *                 that it may be a part of a wider projection's rows */
+typedef struct gdn_norm_shape {
+    int64_t rows, z_stride;
+    int32_t D, heads;
+    int32_t dtype, weight_dtype;
+} gdn_norm_shape;
+
+/* RMS norm of the delta rule's outputs, per value head, times SiLU of a gate:
+ *
+ *   out = x r weight silu(z),   r = 1 / sqrt(mean(x^2) + eps),  silu(z) = z / (1 + e^-z)
+ *
+ *   x, out        [rows, D] dtype;  z  see gdn_norm_shape;  weight [D] weight_dtype
+ *
+ * Tensors are aligned to their element; out must not overlap an input.  The
+ * squares of a row have to sum to a finite fp32.  Returns GDN_OK, GDN_ERR_NULL,
+ * GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or
+ * GDN_ERR_LAUNCH. */
+int gdn_gated_norm(const void *x, const void *z, const void *weight, float eps, void *out,
+                   const gdn_norm_shape *shape, void *stream);
+
+/* The residual stream into a block: with the output x of the block before,
+ *
+ *   hidden = residual + residual_scale x
+ *   out    = hidden r (weight + weight_offset),   r = 1 / sqrt(mean(hidden^2) + eps)
+ *
+ * out is taken from the unrounded hidden.  residual NULL counts as zeros; hidden
+ * NULL is not written, and it may be the residual's buffer.  out must not
+ * overlap anything else.  weight_offset is 1 for weights stored around zero.
+ * Sizes, alignment and statuses as for gdn_gated_norm. */
+int gdn_add_norm(const void *x, const void *residual, const void *weight,
+                 float residual_scale, float weight_offset, float eps,
+                 void *out, void *hidden, const gdn_norm_shape *shape, void *stream);
+
+/* Bytes of device workspace of the two backward passes below: one row of D
+ * floats per workgroup (at most 1024); 0 for invalid sizes or without rows. */
+size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape *shape);
+
+/* Backward pass of gdn_gated_norm.  With n = x r and u = dout weight silu(z):
+ *
+ *   dx = r (u - n mean(n u)),   dz = dout n weight silu'(z),
+ *   dweight = sum over rows of dout n silu(z)
+ *
+ *   dout, dx, dz  [rows, D] contiguous, dtype;  dweight [D] fp32 (zeros without
+ *                 rows), its sum in a fixed order
+ *   workspace     gdn_norm_bwd_workspace_bytes bytes, 16-byte aligned
+ * Outputs must not overlap each other, the inputs or the workspace. */
+int gdn_gated_norm_bwd(const void *x, const void *z, const void *weight, float eps,
+                       const void *dout, void *dx, void *dz, float *dweight,
+                       const gdn_norm_shape *shape, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of gdn_add_norm from its hidden (the forward's output).  With
+ * n = hidden r, u = dout (weight + weight_offset) and dhidden the gradient that
+ * reaches hidden by itself (NULL = zero):
+ *
+ *   dresidual = dhidden + r (u - n mean(n u)),   dx = residual_scale dresidual,
+ *   dweight   = sum over rows of dout n
+ *
+ * dx or dresidual may be NULL (not both): with residual_scale 1 they are equal.
+ * Otherwise as for gdn_gated_norm_bwd. */
+int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, const void *weight,
+                     float residual_scale, float weight_offset, float eps,
+                     void *dx, void *dresidual, float *dweight,
+                     const gdn_norm_shape *shape, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Kernel timing hook, for measurement.  While enabled, every call of the
  * entry points above records HIP events on its stream just before
  * and just after each kernel it enqueues (events are created on first use and
