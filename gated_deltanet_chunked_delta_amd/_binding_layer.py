@@ -2,10 +2,12 @@
 recurrent steps over several tokens, the short causal convolution and the RMS
 norms, forward and backward.
 
-As in ``_binding``: argument marshalling only, no CPU path.  These calls are
-short on a decode batch, so the wrappers keep their own work small: plain
-integers instead of ctypes objects, one struct per call.  A call on another
-device than the current one makes that device current for its duration.
+As in ``_binding``: argument marshalling only, no CPU path.  On a decode batch
+the wrapper's own work is most of a call, so it is kept small: plain integers
+instead of ctypes objects, one struct a call, messages built only when they are
+raised, torch's raw stream handle (0.1 us; ``current_stream`` takes 1.9).  A
+call on another device than the current one makes that device current for its
+duration.
 """
 from __future__ import annotations
 
@@ -14,7 +16,7 @@ import ctypes
 import torch
 
 from . import _binding as _b
-from ._binding import _DTYPES, GDN_OK, GdnError, _check, _gate_inputs, gdn_gates, gdn_shape, gdn_state_pool
+from ._binding import _DTYPES, GdnError, gdn_gates, gdn_shape, gdn_state_pool
 
 EXPORTED_LAYER = ("gdn_recurrent_steps", "gdn_conv_fwd", "gdn_conv_fwd_pool", "gdn_conv_update", "gdn_conv_bwd",
                   "gdn_conv_bwd_workspace_bytes", "gdn_gated_norm", "gdn_gated_norm_bwd", "gdn_add_norm",
@@ -78,8 +80,11 @@ def _r(s):
     return None if s is None else ctypes.addressof(s)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_of(t, stream):
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else int(stream)
+    return _raw_stream(t.get_device()) if stream is None else int(stream)
 
 
 def _bytes(t, nbytes):
@@ -152,26 +157,42 @@ def gdn_add_norm_bwd(dout, dhidden, hidden, weight, residual_scale, weight_offse
                                     _bytes(workspace, workspace_bytes), _stream_of(dout, stream))
 
 
-def _call(fn, *args):
-    """fn(*args) with its first tensor's device current; raises on a bad status."""
-    dev = args[0].device
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args)
+def _run(dev, fn, *args):
+    """fn(*args, stream) with device number dev current; raises on a bad status.
+    The tensors behind the pointers in args are the caller's to keep until then."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args)
-    if st != GDN_OK:
+            st = fn(*args, _raw_stream(dev))
+    if st:
         raise GdnError(st)
 
 
-def _same_device(dev, **tensors):
+def _gpu(x, name):
+    """x's device number and dtype code."""
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU device (there is no CPU path)")
+    return dev, code
+
+
+def _elsewhere(dev, **tensors):
+    """Raises for the first of the tensors that is not on device number dev."""
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}")
 
 
-def _weight_dtype(x, weight, name):
-    _check(weight.dtype == x.dtype or weight.dtype == torch.float32, f"{name} must be {x.dtype} or float32")
+def _weight(x, weight, bias=None):
+    """dtype code of weight and bias: x's dtype or float32."""
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+        raise ValueError(f"weight must be {x.dtype} or float32")
+    if bias is not None and bias.dtype != weight.dtype:
+        raise ValueError(f"bias must be {weight.dtype}")
     return _DTYPES[weight.dtype]
 
 
@@ -182,28 +203,57 @@ def make_step_pool(data, indices, num_accepted=None) -> gdn_step_pool:
                          indices.shape[1] if indices.dim() == 2 else 1, _DTYPES[data.dtype])
 
 
-def _step_pool(data, indices, num_accepted, N, dev, slot, name):
-    """Checks a few-token step's pool, indices [N] or [N, cols] and accepted counts."""
-    _check(data.dim() == 1 + len(slot) and tuple(data.shape[1:]) == slot and data.is_contiguous(),
-           f"{name} must be a contiguous [P,{','.join(map(str, slot))}]")
-    _check(indices.dtype == torch.int32 and indices.dim() in (1, 2) and indices.shape[0] == N
-           and (indices.dim() == 1 or indices.shape[1] > 0), f"{name}'s indices must be int32 [{N}] or [{N},cols]")
-    _check(num_accepted is None or (num_accepted.dtype == torch.int32 and tuple(num_accepted.shape) == (N,)),
-           f"num_accepted must be int32 [{N}]")
-    _same_device(dev, pool=data, indices=indices, num_accepted=num_accepted)
+def _step_pool(dev, data, indices, num_accepted, N, slot, name):
+    """Checks a few-token step's pool, indices [N] or [N, cols] and accepted
+    counts; returns the struct and what it points to."""
+    if data.shape[1:] != slot or not data.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [P,{','.join(map(str, slot))}]")
+    dims = indices.shape
+    if indices.dtype != torch.int32 or not 1 <= len(dims) <= 2 or dims[0] != N or dims[-1] == 0 < N:
+        raise ValueError(f"{name}'s indices must be int32 [{N}] or [{N},cols]")
+    if num_accepted is not None:
+        if num_accepted.dtype != torch.int32 or num_accepted.shape != (N,):
+            raise ValueError(f"num_accepted must be int32 [{N}]")
+        num_accepted = num_accepted.contiguous()
+    if data.get_device() != dev or indices.get_device() != dev or (num_accepted is not None
+                                                                  and num_accepted.get_device() != dev):
+        raise ValueError(f"{name}, its indices and num_accepted must be on cuda:{dev}")
+    indices = indices.contiguous()
+    return make_step_pool(data, indices, num_accepted), (indices, num_accepted)
 
 
-def _sequences(x, cu_seqlens):
-    """Number of sequences of x [B, T, ...]."""
+def _sequences(dev, B, cu_seqlens):
+    """Number of sequences in B rows."""
     if cu_seqlens is None:
-        return x.shape[0]
-    _check(x.shape[0] == 1, "cu_seqlens requires B == 1")
-    _check(cu_seqlens.dim() == 1 and cu_seqlens.dtype == torch.int32 and cu_seqlens.shape[0] > 0,
-           "cu_seqlens must be int32 [N+1]")
-    _check(cu_seqlens.device == x.device, f"cu_seqlens must be on {x.device}")
+        return B
+    if B != 1:
+        raise ValueError("cu_seqlens requires B == 1")
+    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.shape[0] == 0:
+        raise ValueError("cu_seqlens must be int32 [N+1]")
+    if cu_seqlens.get_device() != dev:
+        raise ValueError(f"cu_seqlens must be on cuda:{dev}")
     return cu_seqlens.shape[0] - 1
 
 
+def _given(t, shape, x, dev, name):
+    """Checks a buffer that the caller hands in to be written."""
+    if t.shape != shape or t.dtype != x.dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {x.dtype} {list(shape)} on cuda:{dev}")
+    return t
+
+
+def _workspace(workspace, need, dev, x):
+    """The caller's workspace where it is large enough, else a new one."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous buffer on cuda:{dev}")
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# Recurrent steps
+# ---------------------------------------------------------------------------
 def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_indices, cu_seqlens=None,
                                            num_accepted=None, scale=None, use_qk_l2norm_in_kernel=False, out=None,
                                            A_log=None, dt_bias=None, a_raw=None, b_raw=None):
@@ -220,40 +270,48 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
     state after its last token.  A start slot outside [0, P) marks a padding
     row: zeros in the output, nothing stored.  Returns o with v's shape.
     """
-    _check(q.dim() == 4 and k.shape == q.shape, "q and k must be [B,T,H,K] of equal shape")
-    B, T, H, K = q.shape
-    _check(v.dim() == 4 and v.shape[0] == B and v.shape[1] == T, "v must be [B,T,HV,V]")
-    HV, V = v.shape[2], v.shape[3]
-    dt = q.dtype
-    _check(dt in _DTYPES and k.dtype == dt and v.dtype == dt, "q, k, v must share one dtype (bfloat16 or float32)")
-    _check(q.is_cuda, "tensors must be on a GPU device (there is no CPU path)")
-    dev = q.device
-    N = _sequences(q, cu_seqlens)
-    gates = None
+    dims, vdims, dt = q.shape, v.shape, q.dtype
+    if len(dims) != 4 or k.shape != dims:
+        raise ValueError("q and k must be [B,T,H,K] of equal shape")
+    if len(vdims) != 4 or vdims[:2] != dims[:2]:
+        raise ValueError("v must be [B,T,HV,V]")
+    dev, code = _gpu(q, "q")
+    if k.dtype != dt or v.dtype != dt:
+        raise ValueError("q, k, v must share one dtype (bfloat16 or float32)")
+    B, T, H, K = dims
+    HV, V = vdims[2], vdims[3]
+    N = _sequences(dev, B, cu_seqlens)
+    gates = gp = bp = None
     if g is None and beta is None:
-        A_log, dt_bias, a_raw, b_raw = _gate_inputs(A_log, dt_bias, a_raw, b_raw, (B, T, HV), dt, dev)
-        gates = gdn_gates(A_log.data_ptr(), dt_bias.data_ptr(), a_raw.data_ptr(), b_raw.data_ptr())
+        if A_log is None or dt_bias is None or a_raw is None or b_raw is None:
+            raise ValueError("in-kernel gating needs all of A_log, dt_bias, a_raw, b_raw")
+        if A_log.shape != (HV,) or dt_bias.shape != (HV,) or A_log.dtype != torch.float32 \
+                or dt_bias.dtype != torch.float32:
+            raise ValueError(f"A_log and dt_bias must be float32 [{HV}]")
+        if a_raw.numel() != B * T * HV or b_raw.numel() != B * T * HV or a_raw.dtype != dt or b_raw.dtype != dt:
+            raise ValueError(f"a_raw and b_raw must hold [{B},{T},{HV}] elements of q's dtype")
+        g, beta, A_log, dt_bias = a_raw.contiguous(), b_raw.contiguous(), A_log.contiguous(), dt_bias.contiguous()
+        gates = gdn_gates(A_log.data_ptr(), dt_bias.data_ptr(), g.data_ptr(), beta.data_ptr())
+        _elsewhere(dev, k=k, v=v, A_log=A_log, dt_bias=dt_bias, a_raw=g, b_raw=beta)
     else:
-        _check(g is not None and beta is not None and A_log is None and dt_bias is None and a_raw is None
-               and b_raw is None, "give either g and beta or the raw gate inputs")
-        _check(tuple(g.shape) == (B, T, HV) and g.dtype == torch.float32, "g must be float32 [B,T,HV]")
-        _check(tuple(beta.shape) == (B, T, HV) and beta.dtype == torch.float32, "beta must be float32 [B,T,HV]")
-        _same_device(dev, g=g, beta=beta)
+        if g is None or beta is None or not (A_log is dt_bias is a_raw is b_raw is None):
+            raise ValueError("give either g and beta or the raw gate inputs")
+        if g.shape != vdims[:3] or g.dtype != torch.float32 or beta.shape != vdims[:3] or beta.dtype != torch.float32:
+            raise ValueError("g and beta must be float32 [B,T,HV]")
         g, beta = g.contiguous(), beta.contiguous()
-    _same_device(dev, k=k, v=v)
-    _check(state_pool.dtype in _DTYPES, "state_pool must be float32 or bfloat16")
-    _step_pool(state_pool, state_indices, num_accepted, N, dev, (HV, K, V), "state_pool")
-    if out is None:
-        out = torch.empty((B, T, HV, V), dtype=dt, device=dev)
-    else:
-        _check(out.shape == v.shape and out.dtype == dt and out.is_contiguous() and out.device == dev,
-               f"out must be a contiguous {dt} [{B},{T},{HV},{V}] on {dev}")
-    idx = state_indices.contiguous()
-    acc = None if num_accepted is None else num_accepted.contiguous()
-    cu = None if cu_seqlens is None else cu_seqlens.contiguous()
-    _call(gdn_recurrent_steps, q.contiguous(), k.contiguous(), v.contiguous(), g, beta, gates,
-          K ** -0.5 if scale is None else float(scale), use_qk_l2norm_in_kernel, make_step_pool(state_pool, idx, acc),
-          cu, out, gdn_shape(B, T, H, HV, K, V, N, _DTYPES[dt]))
+        gp, bp = g.data_ptr(), beta.data_ptr()
+        _elsewhere(dev, k=k, v=v, g=g, beta=beta)
+    if state_pool.dtype not in _DTYPES:
+        raise ValueError("state_pool must be float32 or bfloat16")
+    pool, kept = _step_pool(dev, state_pool, state_indices, num_accepted, N, (HV, K, V), "state_pool")
+    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    out = torch.empty_like(v) if out is None else _given(out, vdims, v, dev, "out")
+    if cu_seqlens is not None:
+        cu_seqlens = cu_seqlens.contiguous()
+    shape = gdn_shape(B, T, H, HV, K, V, N, code)
+    _run(dev, (_lib or _load()).gdn_recurrent_steps, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, _r(gates),
+         K ** -0.5 if scale is None else scale, use_qk_l2norm_in_kernel, _r(pool), _p(cu_seqlens), out.data_ptr(),
+         _r(shape))
     return out
 
 
@@ -273,40 +331,55 @@ def _row_stride(x):
 
 
 def _conv_args(x, weight, bias, cu_seqlens, activation):
-    _check(x.dim() == 3 and x.dtype in _DTYPES, "x must be bfloat16 or float32 [B,T,D]")
-    _check(x.is_cuda, "tensors must be on a GPU device (there is no CPU path)")
-    B, T, D = x.shape
-    _check(weight.dim() == 2 and weight.shape[0] == D, f"weight must be [{D},W]")
-    wd = _weight_dtype(x, weight, "weight")
-    _check(bias is None or (tuple(bias.shape) == (D,) and bias.dtype == weight.dtype),
-           f"bias must be {weight.dtype} [{D}]")
-    _check(activation in ("silu", "swish", None), 'activation must be "silu" (or "swish") or None')
-    _same_device(x.device, weight=weight, bias=bias)
-    N = _sequences(x, cu_seqlens)
-    xr, rs = _row_stride(x)
-    shape = gdn_conv_shape(B, T, D, weight.shape[1], N, _DTYPES[x.dtype], wd, max(rs, D))
-    return (xr, weight.contiguous(), None if bias is None else bias.contiguous(),
-            None if cu_seqlens is None else cu_seqlens.contiguous(), shape, N, activation is not None)
+    """Checks and lays out what the convolution's calls share: the device, x's
+    rows, weight, bias, cu_seqlens, the sizes, the number of sequences."""
+    dims = x.shape
+    if len(dims) != 3:
+        raise ValueError("x must be [B,T,D]")
+    dev, code = _gpu(x, "x")
+    B, T, D = dims
+    if weight.dim() != 2 or weight.shape[0] != D:
+        raise ValueError(f"weight must be [{D},W]")
+    if bias is not None:
+        if bias.shape != (D,):
+            raise ValueError(f"bias must be [{D}]")
+        bias = bias.contiguous()
+    wcode = _weight(x, weight, bias)
+    if activation not in ("silu", "swish", None):
+        raise ValueError('activation must be "silu" (or "swish") or None')
+    if weight.get_device() != dev or (bias is not None and bias.get_device() != dev):
+        raise ValueError(f"weight and bias must be on cuda:{dev}")
+    N = _sequences(dev, B, cu_seqlens)
+    if cu_seqlens is not None:
+        cu_seqlens = cu_seqlens.contiguous()
+    rows, rs = _row_stride(x)
+    weight = weight.contiguous()
+    return dev, rows, weight, bias, cu_seqlens, gdn_conv_shape(B, T, D, weight.shape[1], N, code, wcode, rs), N
 
 
-def _conv_out(x, split_sizes, out, name="out"):
-    """The output tensors: given or new, one or one per split size; and their struct."""
+def _pieces(x, sizes, tensors, dev, name):
+    """The output (or its gradient) as one tensor per size, given or new; and their struct."""
     B, T, D = x.shape
-    sizes = (D,) if split_sizes is None else tuple(split_sizes)
-    _check(1 <= len(sizes) <= 3 and min(sizes) >= 0 and sum(sizes) == D,
-           f"split_sizes must be one to three sizes that sum to {D}")
-    if out is None:
-        outs = [torch.empty((B, T, n), dtype=x.dtype, device=x.device) for n in sizes]
-    else:
-        outs = [out] if isinstance(out, torch.Tensor) else list(out)
-        _check(len(outs) == len(sizes), f"{name} must be one tensor per split size")
-        for t, n in zip(outs, sizes):
-            _check(tuple(t.shape) == (B, T, n) and t.dtype == x.dtype and t.is_contiguous() and t.device == x.device,
-                   f"{name} must be contiguous {x.dtype} [{B},{T},{n}] on {x.device}")
+    if not 1 <= len(sizes) <= 3 or sum(sizes) != D or min(sizes) < 0:
+        raise ValueError(f"{name}: one to three sizes that sum to {D} are wanted")
     pieces = gdn_conv_pieces()
-    for i, t in enumerate(outs):
-        pieces.ptr[i], pieces.dim[i] = t.data_ptr(), sizes[i]
-    return outs, pieces
+    if tensors is None:
+        tensors = []
+        for i, n in enumerate(sizes):   # empty_like is the cheaper call: q and k are of one size
+            tensors.append(torch.empty_like(tensors[-1]) if i and n == sizes[i - 1] else x.new_empty((B, T, n)))
+    else:
+        if len(tensors) != len(sizes):
+            raise ValueError(f"{name} must be one tensor per split size")
+        for t, n in zip(tensors, sizes):
+            _given(t, (B, T, n), x, dev, name)
+    ptr, dim = pieces.ptr, pieces.dim
+    for i, t in enumerate(tensors):
+        ptr[i], dim[i] = t.data_ptr(), sizes[i]
+    return tensors, pieces
+
+
+def _listed(out):
+    return None if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
 
 
 def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=True, cu_seqlens=None,
@@ -329,31 +402,36 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
     ``read_initial_state`` is False or the slot is outside the pool) and leaves
     its final state there; the call then returns ``(y, None)``.
     """
-    xr, w, b, cu, shape, N, silu = _conv_args(x, weight, bias, cu_seqlens, activation)
-    slot = (x.shape[2], shape.W - 1)
-    outs, pieces = _conv_out(x, split_sizes, out)
+    dev, rows, weight, bias, cu, shape, N = _conv_args(x, weight, bias, cu_seqlens, activation)
+    D, W1 = x.shape[2], shape.W - 1
+    outs, pieces = _pieces(x, (D,) if split_sizes is None else split_sizes, _listed(out), dev, "out")
     y = outs[0] if split_sizes is None else tuple(outs)
+    lib = _lib or _load()
+    head = (rows.data_ptr(), weight.data_ptr(), _p(bias), activation is not None)
     if conv_state_pool is not None:
-        _check(initial_state is None and final_state is None,
-               "with a state pool, initial and final states live in the pool")
-        _check(conv_state_pool.dtype == x.dtype, f"conv_state_pool must be {x.dtype}")
-        _check(conv_state_indices is not None and conv_state_indices.dim() == 1, f"conv_state_indices must be int32 [{N}]")
-        _step_pool(conv_state_pool, conv_state_indices, None, N, x.device, slot, "conv_state_pool")
-        idx = conv_state_indices.contiguous()
-        _call(gdn_conv_fwd_pool, xr, w, b, silu, _b.make_state_pool(conv_state_pool, idx, read_initial_state), cu,
-              pieces, shape)
+        if initial_state is not None or final_state is not None:
+            raise ValueError("with a state pool, initial and final states live in the pool")
+        if conv_state_pool.dtype != x.dtype:
+            raise ValueError(f"conv_state_pool must be {x.dtype}")
+        if conv_state_indices is None or conv_state_indices.dim() != 1:
+            raise ValueError(f"conv_state_indices must be int32 [{N}]")
+        _, kept = _step_pool(dev, conv_state_pool, conv_state_indices, None, N, (D, W1), "conv_state_pool")
+        pool = _b.make_state_pool(conv_state_pool, kept[0], read_initial_state)
+        _run(dev, lib.gdn_conv_fwd_pool, *head, _r(pool), _p(cu), _r(pieces), _r(shape))
         return y, None
-    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
-        _check(t is None or (tuple(t.shape) == (N, *slot) and t.dtype == x.dtype and t.device == x.device),
-               f"{name} must be {x.dtype} [{N},{slot[0]},{slot[1]}] on {x.device}")
-    _check(final_state is None or final_state.is_contiguous(), "final_state must be contiguous")
     if initial_state is not None:
+        if initial_state.shape != (N, D, W1) or initial_state.dtype != x.dtype or initial_state.get_device() != dev:
+            raise ValueError(f"initial_state must be {x.dtype} [{N},{D},{W1}] on cuda:{dev}")
         initial_state = initial_state.contiguous()
     if not output_final_state:
         final_state = None
-    elif final_state is None:
-        final_state = torch.empty((N, *slot), dtype=x.dtype, device=x.device)
-    _call(gdn_conv_fwd, xr, w, b, silu, initial_state, cu, pieces, final_state, shape)
+    elif final_state is not None:
+        _given(final_state, (N, D, W1), x, dev, "final_state")
+    elif initial_state is not None:
+        final_state = torch.empty_like(initial_state)
+    else:
+        final_state = x.new_empty((N, D, W1))
+    _run(dev, lib.gdn_conv_fwd, *head, _p(initial_state), _p(cu), _r(pieces), _p(final_state), _r(shape))
     return y, final_state
 
 
@@ -370,19 +448,21 @@ def causal_conv1d_update(x, weight, conv_state_pool, conv_state_indices, bias=No
     [..., size] tensors.
     """
     flat = x.dim() == 2
+    out = _listed(out)
     if flat:
-        _check(cu_seqlens is None, "x [N,D] takes one token per sequence")
+        if cu_seqlens is not None:
+            raise ValueError("x [N,D] takes one token per sequence")
         x = x.unsqueeze(1)
-    xr, w, b, cu, shape, N, silu = _conv_args(x, weight, bias, cu_seqlens, activation)
-    _check(conv_state_pool.dtype == x.dtype, f"conv_state_pool must be {x.dtype}")
-    _step_pool(conv_state_pool, conv_state_indices, num_accepted, N, x.device, (x.shape[2], shape.W - 1),
-               "conv_state_pool")
-    if flat and out is not None:
-        out = out.unsqueeze(1) if isinstance(out, torch.Tensor) else [t.unsqueeze(1) for t in out]
-    outs, pieces = _conv_out(x, split_sizes, out)
-    idx = conv_state_indices.contiguous()
-    acc = None if num_accepted is None else num_accepted.contiguous()
-    _call(gdn_conv_update, xr, w, b, silu, make_step_pool(conv_state_pool, idx, acc), cu, pieces, shape)
+        out = None if out is None else [t.unsqueeze(1) for t in out]
+    dev, rows, weight, bias, cu, shape, N = _conv_args(x, weight, bias, cu_seqlens, activation)
+    D = x.shape[2]
+    if conv_state_pool.dtype != x.dtype:
+        raise ValueError(f"conv_state_pool must be {x.dtype}")
+    pool, kept = _step_pool(dev, conv_state_pool, conv_state_indices, num_accepted, N, (D, shape.W - 1),
+                            "conv_state_pool")
+    outs, pieces = _pieces(x, (D,) if split_sizes is None else split_sizes, out, dev, "out")
+    _run(dev, (_lib or _load()).gdn_conv_update, rows.data_ptr(), weight.data_ptr(), _p(bias),
+         activation is not None, _r(pool), _p(cu), _r(pieces), _r(shape))
     if flat:
         outs = [t.squeeze(1) for t in outs]
     return outs[0] if split_sizes is None else tuple(outs)
@@ -398,28 +478,25 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, cu_seqlens=N
     dtype (None unless ``output_dinitial``).  A preallocated uint8 ``workspace``
     of gdn_conv_bwd_workspace_bytes bytes may be given.
     """
-    xr, w, b, cu, shape, N, silu = _conv_args(x, weight, bias, cu_seqlens, activation)
+    dev, rows, weight, bias, cu, shape, N = _conv_args(x, weight, bias, cu_seqlens, activation)
     B, T, D = x.shape
-    dev = x.device
-    dys = [dy] if isinstance(dy, torch.Tensor) else list(dy)
-    _check(all(t.dim() == 3 and t.dtype == x.dtype for t in dys), "dy must have x's dtype and [B,T,...] shapes")
-    dys = [t.contiguous() for t in dys]
-    _, pieces = _conv_out(x, [t.shape[2] for t in dys], dys, "dy")
+    dys = [t.contiguous() for t in _listed(dy)]
+    dys, pieces = _pieces(x, [t.shape[-1] for t in dys], dys, dev, "dy")
     slot = (N, D, shape.W - 1)
     if initial_state is not None:
-        _check(tuple(initial_state.shape) == slot and initial_state.dtype == x.dtype and initial_state.device == dev,
-               f"initial_state must be {x.dtype} [{slot[0]},{slot[1]},{slot[2]}] on {dev}")
+        if initial_state.shape != slot or initial_state.dtype != x.dtype or initial_state.get_device() != dev:
+            raise ValueError(f"initial_state must be {x.dtype} {list(slot)} on cuda:{dev}")
         initial_state = initial_state.contiguous()
-    need = gdn_conv_bwd_workspace_bytes(shape)
-    if workspace is None or _bytes(workspace, None) < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    else:
-        _check(workspace.device == dev and workspace.is_contiguous(), f"workspace must be a contiguous buffer on {dev}")
-    dx = torch.empty((B, T, D), dtype=x.dtype, device=dev)
-    dweight = torch.empty((D, shape.W), dtype=torch.float32, device=dev)
-    dbias = None if bias is None else torch.empty(D, dtype=torch.float32, device=dev)
-    dinitial = torch.empty(slot, dtype=x.dtype, device=dev) if output_dinitial else None
-    _call(gdn_conv_bwd, xr, w, b, silu, initial_state, cu, pieces, dx, dweight, dbias, dinitial, shape, workspace)
+    lib = _lib or _load()
+    need = lib.gdn_conv_bwd_workspace_bytes(_r(shape))
+    ws = _workspace(workspace, need, dev, x)
+    dx = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+    dbias = None if bias is None else torch.empty(D, dtype=torch.float32, device=x.device)
+    dinitial = torch.empty(slot, dtype=x.dtype, device=x.device) if output_dinitial else None
+    _run(dev, lib.gdn_conv_bwd, rows.data_ptr(), weight.data_ptr(), _p(bias), activation is not None,
+         _p(initial_state), _p(cu), _r(pieces), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dinitial), _r(shape),
+         ws.data_ptr(), need)
     return dx, dweight, dbias, dinitial
 
 
@@ -427,56 +504,54 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, cu_seqlens=N
 # RMS norms
 # ---------------------------------------------------------------------------
 def _norm_args(x, weight):
-    _check(x.dim() >= 1 and x.dtype in _DTYPES, "x must be bfloat16 or float32 [...,D]")
-    _check(x.is_cuda, "tensors must be on a GPU device (there is no CPU path)")
-    D = x.shape[-1]
-    _check(weight.dim() == 1 and weight.shape[0] == D, f"weight must be [{D}]")
-    _check(weight.device == x.device, f"weight must be on {x.device}")
-    return gdn_norm_shape(x.numel() // D if D else 0, D, D, 1, _DTYPES[x.dtype], _weight_dtype(x, weight, "weight"))
+    """x's device number, the sizes of its rows, and weight, contiguous."""
+    dev, code = _gpu(x, "x")
+    D = x.shape[-1] if x.dim() else 0
+    if D == 0 or weight.shape != (D,):
+        raise ValueError(f"x must be [...,D] and weight [D], D > 0 (x {list(x.shape)}, weight {list(weight.shape)})")
+    wcode = code if weight.dtype == x.dtype else _weight(x, weight)
+    if weight.get_device() != dev:
+        raise ValueError(f"weight must be on cuda:{dev}")
+    return dev, gdn_norm_shape(x.numel() // D, D, D, 1, code, wcode), weight.contiguous()
 
 
-def _like(x, **tensors):
-    for name, t in tensors.items():
-        _check(t is None or (t.shape == x.shape and t.dtype == x.dtype and t.device == x.device),
-               f"{name} must have x's shape, dtype and device")
+def _same(x, t, name):
+    """t contiguous, after checking it against x."""
+    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
+        raise ValueError(f"{name} must have x's shape, dtype and device")
+    return t.contiguous()
 
 
-def _into(t, x, name):
-    """An output buffer: the caller's, or a new one."""
-    if t is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _like(x, **{name: t})
-    _check(t.is_contiguous(), f"{name} must be contiguous")
-    return t
-
-
-def _gate_rows(z, shape):
+def _gate_rows(x, z, shape):
     """z [..., heads, D] as tokens of heads rows with one stride between them;
     fills in shape, returns z or a contiguous copy."""
+    if z.shape != x.shape or z.dtype != x.dtype or z.get_device() != x.get_device():
+        raise ValueError("z must have x's shape, dtype and device")
     if z.is_contiguous():
         return z
-    D, dims, st = z.shape[-1], z.shape, z.stride()
-    if z.dim() >= 3 and (st[-1] == 1 or D == 1) and (st[-2] == D or dims[-2] == 1):
-        heads, lead = dims[-2], z.dim() - 3
-    elif z.dim() == 2 and (st[-1] == 1 or D == 1):
+    dims, st = z.shape, z.stride()
+    D = dims[-1]
+    if st[-1] != 1 and D != 1:
+        return z.contiguous()
+    # the leading dimensions up to `lead` have to be one run of tokens
+    if len(dims) >= 3 and (st[-2] == D or dims[-2] == 1):
+        heads, lead = dims[-2], len(dims) - 3
+    elif len(dims) == 2:
         heads, lead = 1, 0
     else:
         return z.contiguous()
     zs = st[lead]
-    for i in range(lead):
-        if dims[i] != 1 and st[i] != zs * _prod(dims[i + 1:lead + 1]):
+    run = zs
+    for i in range(lead - 1, -1, -1):
+        run *= dims[i + 1]
+        if dims[i] != 1 and st[i] != run:
             return z.contiguous()
+    if dims[lead] == 1 and lead:
+        return z.contiguous()
     if not heads * D <= zs <= 1 << 31:
         return z.contiguous()
     shape.heads, shape.z_stride = heads, zs
     return z
-
-
-def _prod(dims):
-    n = 1
-    for d in dims:
-        n *= d
-    return n
 
 
 def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
@@ -485,33 +560,29 @@ def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
     x, z [..., D] of one shape and dtype (bf16 or fp32, D up to 1024), as the
     delta rule's output [B,T,HV,V] and its gate, which may be a part of a wider
     projection's rows; weight [D] in x's dtype or float32.  Returns x's shape."""
-    shape = _norm_args(x, weight)
-    _like(x, z=z)
-    out = _into(out, x, "out")
-    _call(gdn_gated_norm, x.contiguous(), _gate_rows(z, shape), weight.contiguous(), float(eps), out, shape)
+    dev, shape, weight = _norm_args(x, weight)
+    z = _gate_rows(x, z, shape)
+    x = x.contiguous()
+    out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
+    _run(dev, (_lib or _load()).gdn_gated_norm, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, out.data_ptr(),
+         _r(shape))
     return out
-
-
-def _norm_workspace(workspace, shape, dev):
-    need = gdn_norm_bwd_workspace_bytes(shape)
-    if workspace is None or _bytes(workspace, None) < need:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _check(workspace.device == dev and workspace.is_contiguous(), f"workspace must be a contiguous buffer on {dev}")
-    return workspace
 
 
 def fused_gated_rms_norm_bwd(x, z, weight, dy, eps=1e-6, workspace=None):
     """Backward pass of ``fused_gated_rms_norm``: ``(dx, dz, dweight)``, dx and
     dz in x's dtype and shape, dweight float32 [D].  A preallocated uint8
     ``workspace`` of gdn_norm_bwd_workspace_bytes bytes may be given."""
-    shape = _norm_args(x, weight)
-    _like(x, z=z, dy=dy)
-    dev = x.device
-    dx, dz = _into(None, x, "dx"), _into(None, x, "dz")
-    dweight = torch.empty(x.shape[-1], dtype=torch.float32, device=dev)
-    zr = _gate_rows(z, shape)
-    _call(gdn_gated_norm_bwd, x.contiguous(), zr, weight.contiguous(), float(eps), dy.contiguous(), dx, dz, dweight,
-          shape, _norm_workspace(workspace, shape, dev))
+    dev, shape, weight = _norm_args(x, weight)
+    z = _gate_rows(x, z, shape)
+    x, dy = x.contiguous(), _same(x, dy, "dy")
+    lib = _lib or _load()
+    need = lib.gdn_norm_bwd_workspace_bytes(_r(shape))
+    ws = _workspace(workspace, need, dev, x)
+    dx, dz = torch.empty_like(x), torch.empty_like(x)
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+    _run(dev, lib.gdn_gated_norm_bwd, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, dy.data_ptr(), dx.data_ptr(),
+         dz.data_ptr(), dweight.data_ptr(), _r(shape), ws.data_ptr(), need)
     return dx, dz, dweight
 
 
@@ -522,12 +593,14 @@ def fused_add_rms_norm(x, residual, weight, eps=1e-6, residual_scale=1.0, weight
     residual may be None (zeros).  Returns ``(y, hidden)``, y = hidden / rms *
     (weight + weight_offset), taken from the unrounded hidden.  ``hidden`` may be
     the residual itself, which is then updated in place."""
-    shape = _norm_args(x, weight)
-    _like(x, residual=residual)
-    out = _into(out, x, "out")
-    hidden = _into(hidden, x, "hidden")
-    _call(gdn_add_norm, x.contiguous(), None if residual is None else residual.contiguous(), weight.contiguous(),
-          float(residual_scale), float(weight_offset), float(eps), out, hidden, shape)
+    dev, shape, weight = _norm_args(x, weight)
+    if residual is not None:
+        residual = _same(x, residual, "residual")
+    x = x.contiguous()
+    out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
+    hidden = torch.empty_like(x) if hidden is None else _given(hidden, x.shape, x, dev, "hidden")
+    _run(dev, (_lib or _load()).gdn_add_norm, x.data_ptr(), _p(residual), weight.data_ptr(), residual_scale,
+         weight_offset, eps, out.data_ptr(), hidden.data_ptr(), _r(shape))
     return out, hidden
 
 
@@ -538,14 +611,18 @@ def fused_add_rms_norm_bwd(dy, dhidden, hidden, weight, eps=1e-6, residual_scale
     ``dy`` and ``dhidden`` (or None) are the gradients of its two outputs.
     Returns ``(dx, dresidual, dweight)`` in the inputs' dtype, dweight float32
     [D]; with residual_scale 1 dx equals dresidual, and ``output_dx=False``
-    leaves it out (None)."""
-    shape = _norm_args(hidden, weight)
-    _like(hidden, dy=dy, dhidden=dhidden)
-    dev = hidden.device
-    dx = _into(None, hidden, "dx") if output_dx else None
-    dresidual = _into(None, hidden, "dresidual")
-    dweight = torch.empty(hidden.shape[-1], dtype=torch.float32, device=dev)
-    _call(gdn_add_norm_bwd, dy.contiguous(), None if dhidden is None else dhidden.contiguous(), hidden.contiguous(),
-          weight.contiguous(), float(residual_scale), float(weight_offset), float(eps), dx, dresidual, dweight, shape,
-          _norm_workspace(workspace, shape, dev))
+    leaves it out (None).  ``workspace`` as for fused_gated_rms_norm_bwd."""
+    dev, shape, weight = _norm_args(hidden, weight)
+    dy = _same(hidden, dy, "dy")
+    if dhidden is not None:
+        dhidden = _same(hidden, dhidden, "dhidden")
+    hidden = hidden.contiguous()
+    lib = _lib or _load()
+    need = lib.gdn_norm_bwd_workspace_bytes(_r(shape))
+    ws = _workspace(workspace, need, dev, hidden)
+    dx = torch.empty_like(hidden) if output_dx else None
+    dresidual = torch.empty_like(hidden)
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=hidden.device)
+    _run(dev, lib.gdn_add_norm_bwd, dy.data_ptr(), _p(dhidden), hidden.data_ptr(), weight.data_ptr(), residual_scale,
+         weight_offset, eps, _p(dx), dresidual.data_ptr(), dweight.data_ptr(), _r(shape), ws.data_ptr(), need)
     return dx, dresidual, dweight

@@ -93,6 +93,11 @@ STEPS = {   # H, HV, K, V, lengths (an int: equal), columns, raw gates, pool typ
     "long": (1, 2, 64, 128, [70, 1], 2, True, F32, True),
     "no_norm": (1, 2, 64, 64, [5, 2, 4], 1, False, BF, False),
     "heads": (4, 4, 64, 64, (2,) * 33, 2, True, F32, True),
+    # 256 heads and more, 2048 and more: wider column splits
+    "many_heads": (2, 8, 128, 128, [i % 5 for i in range(35)], 2, True, F32, True),
+    "many_heads_bf16": (8, 8, 64, 128, (10,) * 33, 1, False, BF, True),
+    "wide": (8, 16, 128, 64, [i % 3 for i in range(131)], 1, True, BF, True),
+    "wide_rows": (16, 16, 64, 128, (2,) * 129, 1, False, BF, True),
 }
 
 
