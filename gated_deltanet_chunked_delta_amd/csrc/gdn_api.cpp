@@ -360,7 +360,7 @@ int check_conv(const gdn_conv_shape *shape, const gdn_conv_pieces *pieces, const
     const int64_t tokens = (int64_t)s.B * s.T;
     if (tokens > INT_MAX - 64 || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
     if (tokens > 0 && s.x_stride < s.D) return GDN_ERR_SHAPE;
-    if (s.x_stride > ((int64_t)1 << 31) || gdn::conv_grid(tokens, s.D, s.N) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (s.x_stride > ((int64_t)1 << 31) || gdn::conv_grid(tokens, s.D, s.N, s.W) > kMaxGrid) return GDN_ERR_SHAPE;
     if (((uintptr_t)cu_seqlens & 3u) != 0) return GDN_ERR_ALIGN;
     if (!pieces) return GDN_ERR_NULL;
     int64_t sum = 0;

@@ -24,8 +24,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kCols = 512;            // columns of a wave
-
 // The largest n < N with cu[n] <= t (0 if none): every lane probes one entry a
 // level.
 __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int t, int T_tot) {
@@ -42,98 +40,86 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int t, int T_t
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// One lane's columns in the pieces of out (or of its gradient).
-template <typename E> struct Piece {
-    E *ptr;              // column 0 of the lane in row 0
-    int64_t stride;      // of its rows
-    bool whole;          // the lane's columns lie in one piece
+// One lane's C columns: of one piece of out (or of its gradient), fewer at the
+// piece's end.  A lane behind the last column reads what the last one reads and
+// stores nothing, so that a wave without piece ends (tails false) loads without a
+// condition.
+template <typename E, int C> struct Lane {
+    int d, m, n;         // first column, columns to read, to store
+    bool tails;
+    E *ptr;              // column d in row 0 of the piece
+    int64_t stride;      // between the piece's rows
+    typedef typename Raw<E, C>::T V;
+    __device__ __forceinline__ Lane(const ConvParams &p, int vec) {
+        int v0 = 0, c0 = 0, total = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) total += (p.piece_dim[i] + C - 1) / C;
+        const int v = min(vec, total - 1);
+        d = m = 0;
+        ptr = nullptr;
+        stride = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int dim = p.piece_dim[i], nv = (dim + C - 1) / C, c = (v - v0) * C;
+            if (v >= v0 && v < v0 + nv) {
+                d = c0 + c;
+                m = min(dim - c, C);
+                ptr = (E *)p.piece[i] + c;
+                stride = dim;
+            }
+            v0 += nv;
+            c0 += dim;
+        }
+        n = vec < total ? m : 0;
+        tails = __any(m < C);
+    }
+    __device__ __forceinline__ V read(const E *p) const { return tails ? load_n<E, C>(p, m, true) : Raw<E, C>::load(p); }
+    __device__ __forceinline__ void write(E *p, const V &v) const { store_n<E, C>(p, v, n, tails); }
+    // row t of the piece; the lane's columns of a row that begins at a uniform address
+    __device__ __forceinline__ E *row(int64_t t) const { return ptr + t * stride; }
+    __device__ __forceinline__ E *in(const void *r) const { return (E *)((char *)r + (unsigned)(d * (int)sizeof(E))); }
 };
-template <typename E> __device__ __forceinline__ Piece<E> piece_of(const ConvParams &p, int d, int n) {
-    int at = 0;
-    Piece<E> r{nullptr, 0, false};
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        if (n > 0 && d >= at && d + n <= at + p.piece_dim[i])
-            r = Piece<E>{(E *)p.piece[i] + (d - at), p.piece_dim[i], true};
-        at += p.piece_dim[i];
-    }
-    return r;
-}
-// Address of one element of the pieces.
-template <typename E> __device__ __forceinline__ E *piece_at(const ConvParams &p, int64_t row, int d) {
-    if (d < p.piece_dim[0]) return (E *)p.piece[0] + row * p.piece_dim[0] + d;
-    d -= p.piece_dim[0];
-    if (d < p.piece_dim[1]) return (E *)p.piece[1] + row * p.piece_dim[1] + d;
-    d -= p.piece_dim[1];
-    return (E *)p.piece[2] + row * p.piece_dim[2] + d;
-}
-template <typename E>
-__device__ __forceinline__ void put_row(const ConvParams &p, const Piece<E> &pc, int64_t row, int d, int n,
-                                        const typename Raw8<E>::T &v) {
-    if (pc.whole) {
-        store_n<E>(pc.ptr + row * pc.stride, v, n);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n) *piece_at<E>(p, row, d + e) = to_e<E>(Raw8<E>::get(v, e));
-}
-template <typename E>
-__device__ __forceinline__ typename Raw8<E>::T get_row(const ConvParams &p, const Piece<E> &pc, int64_t row, int d,
-                                                       int n) {
-    if (pc.whole) return load_n<E>(pc.ptr + row * pc.stride, n);
-    typename Raw8<E>::T v = Raw8<E>::zero();
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n) Raw8<E>::set(v, e, to_f(*piece_at<E>(p, row, d + e)));
-    return v;
-}
 
 // The lane's weights and bias in fp32: w[j][e], b[e].
-template <typename E, int W>
-__device__ __forceinline__ void load_weights(const ConvParams &p, int d, int n, float (*w)[8], float *b) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        b[e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = 0.f;
-    }
-    if (n <= 0) return;
-    // the lane's 8 W weights are consecutive
-    float flat[W * 8];
+template <typename E, int W, int C>
+__device__ __forceinline__ void load_weights(const ConvParams &p, const Lane<E, C> &ln, float (*w)[C], float *b) {
+    // the lane's C W weights are consecutive
+    float flat[W * C];
 #pragma unroll
     for (int j = 0; j < W; ++j)
-        load_w8<E>(p.weight, (int64_t)d * W + j * 8, min(max(n * W - j * 8, 0), 8), p.w_f32, flat + j * 8);
+        load_w<E, C>(p.weight, (int64_t)ln.d * W + j * C, min(max(ln.m * W - j * C, 0), C), ln.tails, p.w_f32, flat + j * C);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < C; ++e) {
+        b[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
-    if (p.bias) load_w8<E>(p.bias, d, n, p.w_f32, b);
+    }
+    if (p.bias) load_w<E, C>(p.bias, ln.d, ln.m, ln.tails, p.w_f32, b);
 }
 
 // A history [D, W-1] at `h`: row j (oldest first) of the lane's columns.
-template <typename E, int W>
-__device__ __forceinline__ void load_history(const E *h, int d, int n, float (*win)[8]) {
-    float flat[(W - 1) * 8];
+template <typename E, int W, int C>
+__device__ __forceinline__ void load_history(const E *h, const Lane<E, C> &ln, float (*win)[C]) {
+    float flat[(W - 1) * C];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        const typename Raw8<E>::T v = load_n<E>(h + (int64_t)d * (W - 1) + j * 8, min(max(n * (W - 1) - j * 8, 0), 8));
+        const auto v = load_n<E, C>(h + (int64_t)ln.d * (W - 1) + j * C, min(max(ln.m * (W - 1) - j * C, 0), C), ln.tails);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) flat[j * 8 + e] = Raw8<E>::get(v, e);
+        for (int e = 0; e < C; ++e) flat[j * C + e] = Raw<E, C>::get(v, e);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) win[j][e] = flat[e * (W - 1) + j];
+        for (int e = 0; e < C; ++e) win[j][e] = flat[e * (W - 1) + j];
 }
-template <typename E, int W>
-__device__ __forceinline__ void store_history(E *h, int d, int n, const float (*win)[8]) {
+template <typename E, int W, int C>
+__device__ __forceinline__ void store_history(E *h, const Lane<E, C> &ln, const float (*win)[C]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        typename Raw8<E>::T v;
+        typename Raw<E, C>::T v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) Raw8<E>::set(v, e, win[(j * 8 + e) % (W - 1)][(j * 8 + e) / (W - 1)]);
-        store_n<E>(h + (int64_t)d * (W - 1) + j * 8, v, min(max(n * (W - 1) - j * 8, 0), 8));
+        for (int e = 0; e < C; ++e) Raw<E, C>::set(v, e, win[(j * C + e) % (W - 1)][(j * C + e) / (W - 1)]);
+        store_n<E, C>(h + (int64_t)ln.d * (W - 1) + j * C, v, min(max(ln.n * (W - 1) - j * C, 0), C), ln.tails);
     }
 }
 
@@ -149,38 +135,74 @@ template <typename E> __device__ __forceinline__ const E *start_of(const ConvPar
     return (const E *)base + s * p.D * (p.W - 1);
 }
 
-// The W-1 rows before token t of a sequence that begins at t0.
-template <typename E, int W>
-__device__ __forceinline__ void load_window(const ConvParams &p, const E *x, int t, int t0, const E *hist, int d, int n,
-                                            float (*win)[8]) {
-    float old[W - 1][8];
+// The W-1 rows before token t (as loaded; rows before the first token are not
+// meant), and the window they give for a sequence that begins at t0.
+template <typename E, int W, int C>
+__device__ __forceinline__ void load_before(const ConvParams &p, const E *x, int t, const Lane<E, C> &ln,
+                                            typename Raw<E, C>::T *v) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) v[j] = ln.read(ln.in(x + (int64_t)max(t - (W - 1) + j, 0) * p.x_stride));
+}
+template <typename E, int W, int C>
+__device__ __forceinline__ void window_of(const ConvParams &p, const typename Raw<E, C>::T *v, int t, int t0,
+                                          const E *hist, const Lane<E, C> &ln, float (*win)[C]) {
+    if (t - t0 >= W - 1) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < C; ++e) win[j][e] = Raw<E, C>::get(v[j], e);
+        return;
+    }
+    float old[W - 1][C];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) old[j][e] = win[j][e] = 0.f;
-    if (hist && t - t0 < W - 1) load_history<E, W>(hist, d, n, old);
+        for (int e = 0; e < C; ++e) old[j][e] = 0.f;
+    if (hist) load_history<E, W, C>(hist, ln, old);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        const int s = t - (W - 1) + j;
-        if (s >= t0) {
-            const typename Raw8<E>::T v = load_n<E>(x + (int64_t)s * p.x_stride, n);
+        // position t - t0 - (W-1) + j: a row, or history row t - t0 + j (constant indices keep it in registers)
+        const bool in = t - t0 + j >= W - 1;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) win[j][e] = Raw8<E>::get(v, e);
-        } else {
-            // position s - t0 in [-(W-1), -1]: history row W-1 + s - t0 (constant indices keep it in registers)
+        for (int e = 0; e < C; ++e) win[j][e] = in ? Raw<E, C>::get(v[j], e) : 0.f;
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i)
-                if (i == W - 1 + s - t0)
+        for (int i = j; i < W - 1; ++i)
+            if (!in && i == t - t0 + j)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) win[j][e] = old[i][e];
-        }
+                for (int e = 0; e < C; ++e) win[j][e] = old[i][e];
     }
 }
 
-template <int W>
-__device__ __forceinline__ void shift_in(float (*win)[8], const float *x) {
+// v[i] for a uniform i < U, by selects of values: registers take constant
+// indices only.
+template <int U, typename V> __device__ __forceinline__ V pick(const V *v, int i) {
+    typedef unsigned words __attribute__((ext_vector_type(sizeof(V) / 4)));
+    words r = __builtin_bit_cast(words, v[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int k = 1; k < U; ++k) {
+        const words o = __builtin_bit_cast(words, v[k]);
+        r = i == k ? o : r;
+    }
+    return __builtin_bit_cast(V, r);
+}
+
+// The sequences as a strip walks them.
+struct Walk {
+    int seq, t0, t1;     // t0 <= the current token < t1
+    // Goes on to the sequence of token r (the strip's first: to the one found for it).
+    __device__ __forceinline__ void to(const ConvParams &p, int r, bool first) {
+        if (!first && seq + 1 < p.N) ++seq;
+        seq_range(p.cu_seqlens, seq, p.T, p.T_tot, t0, t1);
+        while (t1 <= r && seq + 1 < p.N) seq_range(p.cu_seqlens, ++seq, p.T, p.T_tot, t0, t1);
+        if (t1 <= r) t1 = p.T_tot;                    // tokens behind the last sequence's: its own
+        t0 = first ? min(t0, r) : r;
+    }
+};
+
+template <int W, int C>
+__device__ __forceinline__ void shift_in(float (*win)[C], const float *x) {
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
 #pragma unroll
         for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
         win[W - 2][e] = x[e];
@@ -188,138 +210,166 @@ __device__ __forceinline__ void shift_in(float (*win)[8], const float *x) {
 }
 
 // pre-activation of one element
-template <int W>
-__device__ __forceinline__ float pre_of(const float (*w)[8], const float *b, const float (*win)[8], float x, int e) {
+template <int W, int C>
+__device__ __forceinline__ float pre_of(const float (*w)[C], const float *b, const float (*win)[C], float x, int e) {
     float a = b[e];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], win[j][e], a);
     return fmaf(w[W - 1][e], x, a);
 }
 
-// Workgroups [0, nmain): four strips of L tokens by 512 columns.  The ones
-// behind them write final states, one wave per sequence and 512 columns (also
-// of empty sequences); they run in a launch of their own where final_state may
-// be the buffer the strips read histories from.
+// Rows of a load batch: a multiple of W - 1, so that the window's registers are
+// back in place after a batch.
+constexpr int batch_rows(int W) { return W == 4 ? 3 : 4; }
+
+// Workgroups [0, nmain): four strips of L tokens by 64 lanes' columns.  The ones
+// behind them write final states, one wave per sequence and 64 lanes' columns
+// (also of empty sequences); they run in a launch of their own where final_state
+// is the buffer the strips read histories from.
 template <typename E, int W>
 __global__ void __launch_bounds__(256) conv_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
-    typedef Raw8<E> R;
+    constexpr int C = 8, U = batch_rows(W);           // the next batch's loads are in flight
+    typedef Raw<E, C> R;
     typedef typename R::T V;
-    constexpr int U = sizeof(E) == 2 ? 8 : 4;         // rows in flight
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int blk = (int)blockIdx.x;
     if (blk >= nmain) {   // final states
         const int64_t u = (int64_t)(blk - nmain) * 4 + wv;
-        const int s = (int)(u / cblocks), d = (int)(u % cblocks) * kCols + lane * 8, n = min(max(p.D - d, 0), 8);
-        if (s >= p.N || n == 0) return;
+        const int s = (int)(u / cblocks);
+        const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+        if (s >= p.N || ln.n == 0) return;
         E *dst = (E *)start_of<E>(p, s, p.final_state);
         if (!dst) return;
         int t0, t1;
         seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
-        float win[W - 1][8];
-        load_window<E, W>(p, (const E *)p.x + d, t1, t0, start_of<E>(p, s, p.initial), d, n, win);
-        store_history<E, W>(dst, d, n, win);
+        float win[W - 1][C];
+        V before[W - 1];
+        if (t1 > t0) load_before<E, W, C>(p, (const E *)p.x, t1, ln, before);
+        window_of<E, W, C>(p, before, t1, t0, start_of<E>(p, s, p.initial), ln, win);
+        store_history<E, W, C>(dst, ln, win);
         return;
     }
-    const int strip = (blk / cblocks) * 4 + wv, d = (blk % cblocks) * kCols + lane * 8, n = min(max(p.D - d, 0), 8);
+    const int strip = (blk / cblocks) * 4 + wv;
+    const Lane<E, C> ln(p, (blk % cblocks) * 64 + lane);
+    const int n = ln.n;
     if (strip >= nstrips) return;
     const int s0 = strip * L, s1 = min(s0 + L, p.T_tot);
-    int seq = p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T;
+    const E *__restrict__ x = (const E *)p.x;
+    V xa[U], before[W - 1];
+    // rows of one batch, up to the strip's end whatever sequence they belong to
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i < s1) xa[i] = ln.read(ln.in(x + (int64_t)(t + i) * p.x_stride));
+    };
+    load_before<E, W, C>(p, x, s0, ln, before);
+    load(s0);
+    float w[W][C], b[C], win[W - 1][C];
+    load_weights<E, W, C>(p, ln, w, b);
+    Walk at{p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T, 0, 0};
     if (n == 0) return;
-    const E *__restrict__ x = (const E *)p.x + d;
-    const Piece<E> pc = piece_of<E>(p, d, n);
-    float w[W][8], b[8], win[W - 1][8];
-    load_weights<E, W>(p, d, n, w, b);
-    for (int t = s0; t < s1;) {
-        int t0, t1;
-        seq_range(p.cu_seqlens, seq, p.T, p.T_tot, t0, t1);
-        while (t1 <= t && seq + 1 < p.N) seq_range(p.cu_seqlens, ++seq, p.T, p.T_tot, t0, t1);
-        if (t1 <= t) t1 = p.T_tot;                    // tokens behind the last sequence's: its own
-        const int te = min(t1, s1);
-        load_window<E, W>(p, x, t, min(t0, t), start_of<E>(p, seq, p.initial), d, n, win);
-        while (t < te) {
-            V xa[U];
-            const int m = min(te - t, U);
+    auto begin = [&](int r, bool first) {
+        at.to(p, r, first);
+        window_of<E, W, C>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
+    };
+    auto step = [&](int r, const V &v) {
+        float xv[C];
+        V o;
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (i < m) xa[i] = load_n<E>(x + (int64_t)(t + i) * p.x_stride, n);
+        for (int e = 0; e < C; ++e) {
+            xv[e] = R::get(v, e);
+            float a = pre_of<W, C>(w, b, win, xv[e], e);
+            if (p.silu) a *= sigmoid_f(a);
+            R::set(o, e, a);
+        }
+        shift_in<W, C>(win, xv);
+        ln.write(ln.row(r), o);
+    };
+    begin(s0, true);
+    for (int t = s0; t < s1; t += U) {
+        V xc[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (i < m) {
-                    float xv[8];
-                    V o;
+        for (int i = 0; i < U; ++i) xc[i] = xa[i];
+        load(t + U);
+        if (t + U <= at.t1 && t + U <= s1) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        xv[e] = R::get(xa[i], e);
-                        float a = pre_of<W>(w, b, win, xv[e], e);
-                        if (p.silu) a *= sigmoid_f(a);
-                        R::set(o, e, a);
-                    }
-                    shift_in<W>(win, xv);
-                    put_row<E>(p, pc, t + i, d, n, o);
-                }
-            t += m;
+            for (int i = 0; i < U; ++i) step(t + i, xc[i]);
+        } else {   // a sequence or the strip ends in the batch
+#pragma unroll 1
+            for (int r = t; r < min(t + U, s1); ++r) {
+                if (r >= at.t1) begin(r, false);
+                step(r, pick<U>(xc, r - t));
+            }
         }
     }
 }
 
 // A few tokens per sequence with the histories in a pool: one wave per sequence
-// and 512 columns walks the sequence's tokens in order.  It reads the start
-// slot before it stores to any (the slots of a row may be the same).
+// and 64 lanes' columns walks the sequence's tokens in order.  It reads the start
+// slot before it stores to any (the slots of a row may be the same).  Latency
+// counts here, so a lane has four columns: twice the waves of eight at half the
+// registers (156 sequences of six tokens, 640 columns: 5.7 against 6.6 us).
+constexpr int kFewCols = 4;
 template <typename E, int W>
 __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblocks, int64_t units) {
-    typedef Raw8<E> R;
+    constexpr int C = kFewCols, U = 4;
+    typedef Raw<E, C> R;
     typedef typename R::T V;
-    constexpr int U = 4;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t u = (int64_t)blockIdx.x * 4 + wv;
     if (u >= units) return;
-    const int s = (int)(u / cblocks), d = (int)(u % cblocks) * kCols + lane * 8, n = min(max(p.D - d, 0), 8);
-    if (n == 0) return;
+    const int s = (int)(u / cblocks);
+    const StepSlots &sl = p.slots;
+    const int32_t *idx = sl.indices + (int64_t)s * sl.cols;
+    // the first 64 slots of the row in the lanes, looked up while the rows load
+    const int slots = idx[min(lane, sl.cols - 1)];
+    const int a = sl.accepted ? min(max(sl.accepted[s], 1), sl.cols) : 1;
+    const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+    const int n = ln.n;
     int t0, t1;
     seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
     if (t0 == t1) return;
-    const StepSlots &sl = p.slots;
-    const int32_t *idx = sl.indices + (int64_t)s * sl.cols;
-    const int a = sl.accepted ? min(max(sl.accepted[s], 1), sl.cols) : 1;
-    const int slot = idx[a - 1];
-    const Piece<E> pc = piece_of<E>(p, d, n);
+    auto slot_of = [&](int col) { return col < 64 ? __builtin_amdgcn_readlane(slots, col) : idx[col]; };
+    const E *__restrict__ x = (const E *)p.x;
+    V xa[U];
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i < t1) xa[i] = ln.read(ln.in(x + (int64_t)(t + i) * p.x_stride));
+    };
+    load(t0);
+    float w[W][C], b[C], win[W - 1][C];
+    load_weights<E, W, C>(p, ln, w, b);
+    const int slot = slot_of(__builtin_amdgcn_readfirstlane(a) - 1);
     if (slot < 0 || slot >= sl.pool_size) {   // padding row
-        for (int t = t0; t < t1; ++t) put_row<E>(p, pc, t, d, n, R::zero());
+        for (int t = t0; t < t1; ++t) ln.write(ln.row(t), R::zero());
         return;
     }
-    const E *__restrict__ x = (const E *)p.x + d;
     E *pool = (E *)sl.data;
     const int64_t hist = (int64_t)p.D * (W - 1);
-    float w[W][8], b[8], win[W - 1][8];
-    load_history<E, W>(pool + slot * hist, d, n, win);
-    load_weights<E, W>(p, d, n, w, b);
-    for (int t = t0; t < t1;) {
-        V xa[U];
-        const int m = min(t1 - t, U);
+    load_history<E, W, C>(pool + slot * hist, ln, win);
+    for (int t = t0; t < t1; t += U) {
+        if (t > t0) load(t);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (i < m) xa[i] = load_n<E>(x + (int64_t)(t + i) * p.x_stride, n);
+        for (int i = 0; i < U; ++i) {
+            if (t + i >= t1) break;
+            float xv[C];
+            V o;
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (i < m) {
-                float xv[8];
-                V o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    xv[e] = R::get(xa[i], e);
-                    float y = pre_of<W>(w, b, win, xv[e], e);
-                    if (p.silu) y *= sigmoid_f(y);
-                    R::set(o, e, y);
-                }
-                shift_in<W>(win, xv);
-                put_row<E>(p, pc, t + i, d, n, o);
-                const int c = min(t + i - t0, sl.cols - 1);
-                if (c < sl.cols - 1 || t + i == t1 - 1) {
-                    const int to = idx[c];
-                    if (to >= 0 && to < sl.pool_size) store_history<E, W>(pool + to * hist, d, n, win);
-                }
+            for (int e = 0; e < C; ++e) {
+                xv[e] = R::get(xa[i], e);
+                float y = pre_of<W, C>(w, b, win, xv[e], e);
+                if (p.silu) y *= sigmoid_f(y);
+                R::set(o, e, y);
             }
-        t += m;
+            shift_in<W, C>(win, xv);
+            ln.write(ln.row(t + i), o);
+            const int c = min(t + i - t0, sl.cols - 1);
+            if (c < sl.cols - 1 || t + i == t1 - 1) {
+                const int to = slot_of(c);
+                if (to >= 0 && to < sl.pool_size) store_history<E, W, C>(pool + to * hist, ln, win);
+            }
+        }
     }
 }
 
@@ -329,153 +379,200 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
 // and the same for the history rows.  A strip walks its tokens and the W-1
 // behind them, computing pre again; the sums of dx for the last W-1 tokens are
 // kept in registers until complete.  The four strips of a workgroup add their
-// dweight and dbias through LDS into one row of the workspace.
+// dweight and dbias through LDS into one row of the workspace.  A lane has four
+// columns: windows, weights and sums are 4 W + 1 floats a column, and with eight
+// columns one or two waves are left a SIMD to hide the loads behind (16,384
+// tokens of 8192 columns 246 us, with four 191; three waves a SIMD instead of two
+// another 8 % where the tokens do not fill the card evenly).
+constexpr int kBwdCols = 4;
+
 template <typename E, int W>
-__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
-    typedef Raw8<E> R;
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
+conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
+    constexpr int C = kBwdCols, U = batch_rows(W);
+    typedef Raw<E, C> R;
     typedef typename R::T V;
-    constexpr int U = sizeof(E) == 2 ? 4 : 2;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int blk = (int)blockIdx.x;
     if (blk >= nmain) {   // gradients of the start histories
         const int64_t u = (int64_t)(blk - nmain) * 4 + wv;
-        const int s = (int)(u / cblocks), d = (int)(u % cblocks) * kCols + lane * 8, n = min(max(p.D - d, 0), 8);
+        const int s = (int)(u / cblocks);
+        const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+        const int n = ln.n;
         if (s >= p.N || n == 0) return;
         int t0, t1;
         seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
-        const E *x = (const E *)p.x + d;
-        const Piece<E> pc = piece_of<E>(p, d, n);
-        float w[W][8], b[8], win[W - 1][8], g[W - 1][8];
-        load_weights<E, W>(p, d, n, w, b);
-        load_window<E, W>(p, x, t0, t0, start_of<E>(p, s, p.initial), d, n, win);
+        const E *x = (const E *)p.x;
+        float w[W][C], b[C], win[W - 1][C], g[W - 1][C];
+        load_weights<E, W, C>(p, ln, w, b);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = 0.f;
+            for (int e = 0; e < C; ++e) g[i][e] = win[i][e] = 0.f;
+        if (const E *h = start_of<E>(p, s, p.initial)) load_history<E, W, C>(h, ln, win);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
             if (t0 + i < t1) {
-                const V xa = load_n<E>(x + (int64_t)(t0 + i) * p.x_stride, n), da = get_row<E>(p, pc, t0 + i, d, n);
-                float xv[8];
+                const V xa = ln.read(ln.in(x + (int64_t)(t0 + i) * p.x_stride)), da = ln.read(ln.row(t0 + i));
+                float xv[C];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < C; ++e) {
                     xv[e] = R::get(xa, e);
-                    const float a = pre_of<W>(w, b, win, xv[e], e);
+                    const float a = pre_of<W, C>(w, b, win, xv[e], e);
                     const float sg = sigmoid_f(a);
                     const float dp = R::get(da, e) * (p.silu ? sg * fmaf(a, 1.f - sg, 1.f) : 1.f);
                     // token i uses history row r with weight r - i
 #pragma unroll
                     for (int r = i; r < W - 1; ++r) g[r][e] = fmaf(w[r - i][e], dp, g[r][e]);
                 }
-                shift_in<W>(win, xv);
+                shift_in<W, C>(win, xv);
             }
-        store_history<E, W>((E *)p.dinitial + (int64_t)s * p.D * (W - 1), d, n, g);
+        store_history<E, W, C>((E *)p.dinitial + (int64_t)s * p.D * (W - 1), ln, g);
         return;
     }
-    __shared__ float red[4][(W + 1) * kCols];
-    const int group = blk / cblocks, c0 = (blk % cblocks) * kCols;
-    const int strip = group * 4 + wv, d = c0 + lane * 8, n = min(max(p.D - d, 0), 8);
-    float dw[W + 1][8];
+    __shared__ float red[4][W + 1][64 * C];
+    const int group = blk / cblocks, strip = group * 4 + wv;
+    const Lane<E, C> ln(p, (blk % cblocks) * 64 + lane);
+    const int n = ln.n;
+    float dw[W + 1][C];
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
+        for (int e = 0; e < C; ++e) dw[j][e] = 0.f;
     if (strip < nstrips) {
-        const int s0 = strip * L, s1 = min(s0 + L, p.T_tot);
-        int seq = p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T;
-        const E *__restrict__ x = (const E *)p.x + d;
-        E *__restrict__ dx = (E *)p.dx + d;
-        const Piece<E> pc = piece_of<E>(p, d, n);
-        float w[W][8], b[8], win[W - 1][8], acc[W - 1][8];
-        load_weights<E, W>(p, d, n, w, b);
-        for (int t = s0; t < s1 && n > 0;) {
-            int t0, t1;
-            seq_range(p.cu_seqlens, seq, p.T, p.T_tot, t0, t1);
-            while (t1 <= t && seq + 1 < p.N) seq_range(p.cu_seqlens, ++seq, p.T, p.T_tot, t0, t1);
-            if (t1 <= t) t1 = p.T_tot;
-            const int ta = t, tb = min(t1, s1), te = min(t1, tb + W - 1);
-            load_window<E, W>(p, x, t, min(t0, t), start_of<E>(p, seq, p.initial), d, n, win);
+        const int s0 = strip * L, s1 = min(s0 + L, p.T_tot), se = min(s1 + W - 1, p.T_tot);
+        const E *__restrict__ x = (const E *)p.x;
+        E *__restrict__ dx = (E *)p.dx;
+        V xa[U], da[U], before[W - 1];
+        auto load = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (t + i < se) {
+                    xa[i] = ln.read(ln.in(x + (int64_t)(t + i) * p.x_stride));
+                    da[i] = ln.read(ln.row(t + i));
+                }
+        };
+        load_before<E, W, C>(p, x, s0, ln, before);
+        load(s0);
+        float w[W][C], b[C], win[W - 1][C], acc[W - 1][C];
+        load_weights<E, W, C>(p, ln, w, b);
+        Walk at{p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T, 0, 0};
+        int ta = s0;                                   // the sequence's first token in the strip
+        auto put = [&](int row, const float *v) {
+            V o;
+#pragma unroll
+            for (int e = 0; e < C; ++e) R::set(o, e, v[e]);
+            ln.write(ln.in(dx + (int64_t)row * p.D), o);
+        };
+        auto begin = [&](int r, bool first) {
+            at.to(p, r, first);
+            ta = r;
+            window_of<E, W, C>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[j][e] = 0.f;
-            auto put = [&](int row, const float *v) {
-                V o;
+                for (int e = 0; e < C; ++e) acc[j][e] = 0.f;
+        };
+        // own: 0 for a row behind the strip, which counts for another one's dweight
+        auto step = [&](int r, const V &xr, const V &dr, float own) {
+            float xv[C], whole[C];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) R::set(o, e, v[e]);
-                store_n<E>(dx + (int64_t)row * p.D, o, n);
-            };
-            while (t < te) {
-                V xa[U], da[U];
-                const int m = min(te - t, U);
+            for (int e = 0; e < C; ++e) {
+                xv[e] = R::get(xr, e);
+                const float a = pre_of<W, C>(w, b, win, xv[e], e);
+                const float sg = sigmoid_f(a);
+                const float dp = R::get(dr, e) * (p.silu ? sg * fmaf(a, 1.f - sg, 1.f) : 1.f), dpo = dp * own;
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (i < m) {
-                        xa[i] = load_n<E>(x + (int64_t)(t + i) * p.x_stride, n);
-                        da[i] = get_row<E>(p, pc, t + i, d, n);
-                    }
+                for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(dpo, win[j][e], dw[j][e]);
+                dw[W - 1][e] = fmaf(dpo, xv[e], dw[W - 1][e]);
+                dw[W][e] += dpo;
+                // weight j reaches token r - (W-1) + j
+                whole[e] = fmaf(w[0][e], dp, acc[0][e]);
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (i < m) {
-                        const bool own = t + i < tb;
-                        float xv[8], dp[8], done[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            xv[e] = R::get(xa[i], e);
-                            const float a = pre_of<W>(w, b, win, xv[e], e);
-                            const float sg = sigmoid_f(a);
-                            dp[e] = R::get(da[i], e) * (p.silu ? sg * fmaf(a, 1.f - sg, 1.f) : 1.f);
-                            if (own) {
-#pragma unroll
-                                for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(dp[e], win[j][e], dw[j][e]);
-                                dw[W - 1][e] = fmaf(dp[e], xv[e], dw[W - 1][e]);
-                                dw[W][e] += dp[e];
-                            }
-                            // weight j reaches token t - (W-1) + j
-                            done[e] = fmaf(w[0][e], dp[e], acc[0][e]);
-#pragma unroll
-                            for (int j = 0; j + 1 < W - 1; ++j) acc[j][e] = fmaf(w[j + 1][e], dp[e], acc[j + 1][e]);
-                            acc[W - 2][e] = w[W - 1][e] * dp[e];
-                        }
-                        shift_in<W>(win, xv);
-                        if (t + i - (W - 1) >= ta) put(t + i - (W - 1), done);
-                    }
-                t += m;
+                for (int j = 0; j + 1 < W - 1; ++j) acc[j][e] = fmaf(w[j + 1][e], dp, acc[j + 1][e]);
+                acc[W - 2][e] = w[W - 1][e] * dp;
             }
-            if (te == t1) {   // the sequence ends: its last tokens' sums are complete
+            shift_in<W, C>(win, xv);
+            if (r - (W - 1) >= ta) put(r - (W - 1), whole);
+        };
+        if (n > 0) {
+            begin(s0, true);
+            for (int t = s0; t < se; t += U) {
+                V xc[U], dc[U];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    const int row = t1 - (W - 1) + j;
-                    if (row >= ta && row < tb) put(row, acc[j]);
+                for (int i = 0; i < U; ++i) {
+                    xc[i] = xa[i];
+                    dc[i] = da[i];
                 }
+                load(t + U);
+                if (t + U < at.t1 && t + U <= s1) {
+#pragma unroll
+                    for (int i = 0; i < U; ++i) step(t + i, xc[i], dc[i], 1.f);
+                    continue;
+                }
+                // a sequence or the strip ends in the batch
+                int r = t;
+#pragma unroll 1
+                for (; r < min(t + U, se); ++r) {
+                    if (r >= at.t1) {
+                        if (r >= s1) break;            // nothing of the strip's sequences is left
+                        begin(r, false);
+                    }
+                    step(r, pick<U>(xc, r - t), pick<U>(dc, r - t), r < s1 ? 1.f : 0.f);
+                    if (r + 1 == at.t1) {              // the sequence ends: its last tokens' sums are whole
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) {
+                            const int row = at.t1 - (W - 1) + j;
+                            if (row >= ta && row < s1) put(row, acc[j]);
+                        }
+                    }
+                }
+                if (r >= at.t1 && r >= s1) break;
             }
-            t = tb;
         }
     }
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[wv][j * kCols + lane * 8 + e] = dw[j][e];
+        for (int e = 0; e < C; ++e) red[wv][j][lane * C + e] = dw[j][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < (W + 1) * kCols; i += 256) {
-        const int j = i / kCols, c = c0 + i % kCols;
-        if (c < p.D)
-            p.part[((int64_t)group * (W + 1) + j) * p.D + c] = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
-    }
+    for (int j = wv; j <= W; j += 4)
+#pragma unroll
+        for (int e = 0; e < C; ++e)
+            if (e < n) {
+                const int c = lane * C + e;
+                p.part[((int64_t)group * (W + 1) + j) * p.D + ln.d + e] =
+                    (red[0][j][c] + red[1][j][c]) + (red[2][j][c] + red[3][j][c]);
+            }
 }
 
-int64_t col_blocks(int64_t D) { return (D + kCols - 1) / kCols; }
-// Tokens of a strip: long enough that the W-1 rows read twice are few, short
-// enough for about 8192 waves.
-int strip_len(int64_t T_tot, int64_t D, int lo, int hi) {
+int64_t col_blocks(int64_t D, int C) { return (D + 64 * C - 1) / (64 * C); }
+// Blocks of 64 lanes over the pieces' vectors (each piece starts a vector).
+int lane_blocks(const ConvParams &p, int C) {
+    int64_t v = 0;
+    for (int i = 0; i < 3; ++i) v += ((int64_t)p.piece_dim[i] + C - 1) / C;
+    return (int)((v + 63) / 64);
+}
+constexpr int kStripWaves = 4096;
+// Tokens of a strip: whole load batches, long enough that the W-1 rows read
+// twice are few, short enough for 4096 waves.
+int strip_len(int64_t T_tot, int64_t D, int C, int lo, int hi) {
     int L = hi;
-    while (L > lo && ((T_tot + L - 1) / L) * col_blocks(D) < 8192) L >>= 1;
+    while (L > lo && ((T_tot + L - 1) / L) * col_blocks(D, C) < kStripWaves) L >>= 1;
     return L;
+}
+int fwd_strip(int64_t T_tot, int64_t D, int W) { return strip_len(T_tot, D, 8, batch_rows(W), 8 * batch_rows(W)); }
+int bwd_strip(int64_t T_tot, int64_t D, int W) {
+    return strip_len(T_tot, D, kBwdCols, batch_rows(W), 32 * batch_rows(W));
+}
+int bwd_groups(int64_t T_tot, int64_t D, int W) {
+    const int64_t L = bwd_strip(T_tot, D, W), strips = (T_tot + L - 1) / L;
+    return (int)((strips + 3) / 4);
 }
 
 template <typename E, int W>
 void launch_fwd_cfg(const ConvParams &p, hipStream_t st, Profiler *prof) {
-    const int L = strip_len(p.T_tot, p.D, 4, 32), cb = (int)col_blocks(p.D);
+    const int L = fwd_strip(p.T_tot, p.D, W), cb = lane_blocks(p, 8);
     const int nstrips = (p.T_tot + L - 1) / L, nmain = (nstrips + 3) / 4 * cb;
     const int nfin = p.final_state ? (int)(((int64_t)p.N * cb + 3) / 4) : 0;
     // final states written over the start histories wait for every strip
@@ -488,14 +585,14 @@ void launch_fwd_cfg(const ConvParams &p, hipStream_t st, Profiler *prof) {
 
 template <typename E, int W>
 void launch_update_cfg(const ConvParams &p, hipStream_t st) {
-    const int cb = (int)col_blocks(p.D);
+    const int cb = lane_blocks(p, kFewCols);
     const int64_t units = (int64_t)p.N * cb;
     conv_update_kernel<E, W><<<(unsigned)((units + 3) / 4), 256, 0, st>>>(p, cb, units);
 }
 
 template <typename E, int W>
 void launch_bwd_cfg(const ConvParams &p, int L, hipStream_t st) {
-    const int cb = (int)col_blocks(p.D);
+    const int cb = lane_blocks(p, kBwdCols);
     const int nstrips = (p.T_tot + L - 1) / L, nmain = (nstrips + 3) / 4 * cb;
     const int nfin = p.dinitial ? (int)(((int64_t)p.N * cb + 3) / 4) : 0;
     conv_bwd_kernel<E, W><<<nmain + nfin, 256, 0, st>>>(p, L, nstrips, cb, nmain);
@@ -507,17 +604,11 @@ template <typename F> void for_width(int W, F f) {
     if (W == 4) f(std::integral_constant<int, 4>{});
 }
 
-int bwd_strip(int64_t T_tot, int64_t D) { return strip_len(T_tot, D, 8, 64); }
-int bwd_groups(int64_t T_tot, int64_t D) {
-    const int64_t L = bwd_strip(T_tot, D), strips = (T_tot + L - 1) / L;
-    return (int)((strips + 3) / 4);
-}
-
 }  // namespace
 
-int64_t conv_grid(int64_t T_tot, int64_t D, int64_t N) {
-    const int64_t L = strip_len(T_tot, D, 4, 32);
-    return ((T_tot + L - 1) / L + 3) / 4 * col_blocks(D) + (N * col_blocks(D) + 3) / 4;
+int64_t conv_grid(int64_t T_tot, int64_t D, int64_t N, int W) {
+    const int64_t L = fwd_strip(T_tot, D, W), cb = col_blocks(D + 16, 8);   // three pieces: at most two vectors more
+    return ((T_tot + L - 1) / L + 3) / 4 * cb + (N * cb + 3) / 4;
 }
 
 hipError_t launch_conv(const ConvParams &p, int dtype, hipStream_t stream, Profiler *prof) {
@@ -542,11 +633,11 @@ hipError_t launch_conv_update(const ConvParams &p, int dtype, hipStream_t stream
 }
 
 size_t conv_bwd_workspace_bytes(int64_t T_tot, int D, int W) {
-    return (size_t)bwd_groups(T_tot, D) * (W + 1) * D * 4;
+    return (size_t)bwd_groups(T_tot, D, W) * (W + 1) * D * 4;
 }
 
 hipError_t launch_conv_bwd(const ConvParams &p, int dtype, hipStream_t stream, Profiler *prof) {
-    const int L = bwd_strip(p.T_tot, p.D);
+    const int L = bwd_strip(p.T_tot, p.D, p.W);
     if (p.T_tot > 0 || (p.N > 0 && p.dinitial)) {
         if (prof) prof->begin(kConvBwdKernel, stream);
         for_width(p.W, [&](auto w) {
@@ -557,7 +648,7 @@ hipError_t launch_conv_bwd(const ConvParams &p, int dtype, hipStream_t stream, P
         if (prof) prof->end(kConvBwdKernel, stream);
         if (err != hipSuccess) return err;
     }
-    return launch_column_sum(p.part, bwd_groups(p.T_tot, p.D), (int64_t)(p.W + 1) * p.D, p.dweight, p.D, p.W, p.dbias,
+    return launch_column_sum(p.part, bwd_groups(p.T_tot, p.D, p.W), (int64_t)(p.W + 1) * p.D, p.dweight, p.D, p.W, p.dbias,
                              stream, prof);
 }
 

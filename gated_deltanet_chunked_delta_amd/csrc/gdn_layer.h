@@ -67,7 +67,7 @@ hipError_t launch_conv_update(const ConvParams &p, int dtype, hipStream_t stream
 size_t conv_bwd_workspace_bytes(int64_t T_tot, int D, int W);
 hipError_t launch_conv_bwd(const ConvParams &p, int dtype, hipStream_t stream, Profiler *prof);
 // Workgroups of the largest grid these sizes launch (host check against the grid limit).
-int64_t conv_grid(int64_t T_tot, int64_t D, int64_t N);
+int64_t conv_grid(int64_t T_tot, int64_t D, int64_t N, int W);
 
 // The RMS norms.  gated: y = x r w silu(z); else h = residual + alpha x,
 // y = h r (w + offset), r = (mean of squares + eps)^-1/2.

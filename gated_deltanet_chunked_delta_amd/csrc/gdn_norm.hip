@@ -57,12 +57,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
     E *hid = (E *)p.hidden;
     const int D = p.D;
     const float inv = 1.f / (float)D;
+    const bool tails = D % 8 != 0;
     float w[NV][8];
     int n[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         n[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w8<E>(p.weight, (i * L + l) * 8, n[i], p.w_f32, w[i]);
+        load_w<E>(p.weight, (i * L + l) * 8, n[i], tails, p.w_f32, w[i]);
         if (!GATED)
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[i][e] += p.offset;
@@ -75,11 +76,11 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i]);
+            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i], tails);
             if (GATED)
-                za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i]);
+                za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i], tails);
             else if (res)
-                za[i] = load_n<E>(res + at + (i * L + l) * 8, n[i]);
+                za[i] = load_n<E>(res + at + (i * L + l) * 8, n[i], tails);
         }
     };
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
@@ -109,9 +110,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                 R::set(o, e, v);
                 if (!GATED) R::set(ho, e, h[i][e]);
             }
-            store_n<E>(y + at + (i * L + l) * 8, o, n[i]);
+            store_n<E>(y + at + (i * L + l) * 8, o, n[i], tails);
             if (!GATED)
-                if (hid) store_n<E>(hid + at + (i * L + l) * 8, ho, n[i]);
+                if (hid) store_n<E>(hid + at + (i * L + l) * 8, ho, n[i], tails);
         }
     }
 }
@@ -130,12 +131,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
     E *__restrict__ dx = (E *)p.dx, *__restrict__ dz = (E *)(GATED ? p.dz : p.dresidual);
     const int D = p.D;
     const float inv = 1.f / (float)D;
+    const bool tails = D % 8 != 0;
     float w[NV][8], dw[NV][8];
     int n[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         n[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w8<E>(p.weight, (i * L + l) * 8, n[i], p.w_f32, w[i]);
+        load_w<E>(p.weight, (i * L + l) * 8, n[i], tails, p.w_f32, w[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (!GATED) w[i][e] += p.offset;
@@ -150,9 +152,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i]);
-            da[i] = load_n<E>(dy + at + (i * L + l) * 8, n[i]);
-            if (GATED || z) za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i]);
+            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i], tails);
+            da[i] = load_n<E>(dy + at + (i * L + l) * 8, n[i], tails);
+            if (GATED || z) za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i], tails);
         }
     };
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
@@ -194,8 +196,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                     R::set(o, e, p.alpha * d);
                 }
             }
-            if (GATED || dx) store_n<E>(dx + at + (i * L + l) * 8, o, n[i]);
-            if (GATED || dz) store_n<E>(dz + at + (i * L + l) * 8, oz, n[i]);
+            if (GATED || dx) store_n<E>(dx + at + (i * L + l) * 8, o, n[i], tails);
+            if (GATED || dz) store_n<E>(dz + at + (i * L + l) * 8, oz, n[i], tails);
         }
     }
     // the workgroup's sums of dw: over its groups in order
@@ -222,21 +224,25 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
     }
 }
 
-// Sum of n rows of `cols` floats: sixteen columns by 64 row lanes a workgroup;
-// each row lane adds its rows in order, then the row lanes are added in a tree,
-// so the result does not depend on scheduling.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ part, int n, int64_t cols,
-                                                          float *__restrict__ out, int D, int W,
-                                                          float *__restrict__ out2) {
-    __shared__ float red[64][17];
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 16 + cl;
+// Sum of n rows of `cols` floats: CL columns by RL row lanes a workgroup; each row
+// lane adds its rows in order, then the row lanes are added in a tree, so the
+// result does not depend on scheduling.
+template <int CL, int RL>
+__global__ void __launch_bounds__(CL * RL) column_sum_kernel(const float *__restrict__ part, int n, int64_t cols,
+                                                             float *__restrict__ out, int D, int W,
+                                                             float *__restrict__ out2) {
+    __shared__ float red[RL][CL + 1];
+    const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+    const int64_t c = (int64_t)blockIdx.x * CL + cl;
     float s = 0.f;
-    if (c < cols)
-        for (int i = rl; i < n; i += 64) s += part[i * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = rl; i < n; i += RL) s += part[i * cols + c];
+    }
     red[rl][cl] = s;
     __syncthreads();
-    for (int h = 32; h >= 1; h >>= 1) {
+#pragma unroll
+    for (int h = RL / 2; h >= 1; h >>= 1) {
         if (rl < h) red[rl][cl] += red[rl + h][cl];
         __syncthreads();
     }
@@ -319,7 +325,11 @@ hipError_t launch_column_sum(const float *part, int n, int64_t cols, float *out,
                              hipStream_t stream, Profiler *prof) {
     if (cols == 0) return hipSuccess;
     if (prof) prof->begin(kColumnSumKernel, stream);
-    column_sum_kernel<<<(unsigned)((cols + 15) / 16), 1024, 0, stream>>>(part, n, cols, out, D, W, out2);
+    // few columns: many row lanes, so that the rows are not a long chain of loads
+    if (cols <= 8192)
+        column_sum_kernel<16, 64><<<(unsigned)((cols + 15) / 16), 1024, 0, stream>>>(part, n, cols, out, D, W, out2);
+    else
+        column_sum_kernel<64, 4><<<(unsigned)((cols + 63) / 64), 256, 0, stream>>>(part, n, cols, out, D, W, out2);
     const hipError_t err = hipGetLastError();
     if (prof) prof->end(kColumnSumKernel, stream);
     return err;

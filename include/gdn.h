@@ -532,7 +532,8 @@ int gdn_conv_update(const void *x, const void *weight, const void *bias, int sil
                     const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream);
 
 /* Bytes of device workspace gdn_conv_bwd needs: W + 1 floats per column for
- * each block of 32 to 256 tokens; 0 for invalid sizes or without tokens. */
+ * each block of 12 to 512 tokens (the more tokens and columns, the longer); 0
+ * for invalid sizes or without tokens. */
 size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape);
 
 /* Backward pass of gdn_conv_fwd (training).  With dpre = dout silu'(pre),
