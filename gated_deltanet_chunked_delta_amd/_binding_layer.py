@@ -81,6 +81,7 @@ def _r(s):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_addr = ctypes.addressof
 
 
 def _stream_of(t, stream):
@@ -180,13 +181,6 @@ def _gpu(x, name):
     return dev, code
 
 
-def _elsewhere(dev, **tensors):
-    """Raises for the first of the tensors that is not on device number dev."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on cuda:{dev}")
-
-
 def _weight(x, weight, bias=None):
     """dtype code of weight and bias: x's dtype or float32."""
     if weight.dtype != x.dtype and weight.dtype != torch.float32:
@@ -206,20 +200,24 @@ def make_step_pool(data, indices, num_accepted=None) -> gdn_step_pool:
 def _step_pool(dev, data, indices, num_accepted, N, slot, name):
     """Checks a few-token step's pool, indices [N] or [N, cols] and accepted
     counts; returns the struct and what it points to."""
+    dims, acc = indices.shape, None
     if data.shape[1:] != slot or not data.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [P,{','.join(map(str, slot))}]")
-    dims = indices.shape
     if indices.dtype != torch.int32 or not 1 <= len(dims) <= 2 or dims[0] != N or dims[-1] == 0 < N:
         raise ValueError(f"{name}'s indices must be int32 [{N}] or [{N},cols]")
     if num_accepted is not None:
         if num_accepted.dtype != torch.int32 or num_accepted.shape != (N,):
             raise ValueError(f"num_accepted must be int32 [{N}]")
+        if num_accepted.get_device() != dev:
+            raise ValueError(f"num_accepted must be on cuda:{dev}")
         num_accepted = num_accepted.contiguous()
-    if data.get_device() != dev or indices.get_device() != dev or (num_accepted is not None
-                                                                  and num_accepted.get_device() != dev):
-        raise ValueError(f"{name}, its indices and num_accepted must be on cuda:{dev}")
+        acc = num_accepted.data_ptr()
+    if data.get_device() != dev or indices.get_device() != dev:
+        raise ValueError(f"{name} and its indices must be on cuda:{dev}")
     indices = indices.contiguous()
-    return make_step_pool(data, indices, num_accepted), (indices, num_accepted)
+    pool = gdn_step_pool(data.data_ptr(), indices.data_ptr(), acc, data.shape[0], dims[1] if len(dims) == 2 else 1,
+                         _DTYPES[data.dtype])
+    return pool, (indices, num_accepted)
 
 
 def _sequences(dev, B, cu_seqlens):
@@ -292,7 +290,8 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
             raise ValueError(f"a_raw and b_raw must hold [{B},{T},{HV}] elements of q's dtype")
         g, beta, A_log, dt_bias = a_raw.contiguous(), b_raw.contiguous(), A_log.contiguous(), dt_bias.contiguous()
         gates = gdn_gates(A_log.data_ptr(), dt_bias.data_ptr(), g.data_ptr(), beta.data_ptr())
-        _elsewhere(dev, k=k, v=v, A_log=A_log, dt_bias=dt_bias, a_raw=g, b_raw=beta)
+        if A_log.get_device() != dev or dt_bias.get_device() != dev:
+            raise ValueError(f"A_log and dt_bias must be on cuda:{dev}")
     else:
         if g is None or beta is None or not (A_log is dt_bias is a_raw is b_raw is None):
             raise ValueError("give either g and beta or the raw gate inputs")
@@ -300,7 +299,8 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
             raise ValueError("g and beta must be float32 [B,T,HV]")
         g, beta = g.contiguous(), beta.contiguous()
         gp, bp = g.data_ptr(), beta.data_ptr()
-        _elsewhere(dev, k=k, v=v, g=g, beta=beta)
+    if not k.get_device() == v.get_device() == g.get_device() == beta.get_device() == dev:
+        raise ValueError(f"k, v and the gates must be on cuda:{dev}")
     if state_pool.dtype not in _DTYPES:
         raise ValueError("state_pool must be float32 or bfloat16")
     pool, kept = _step_pool(dev, state_pool, state_indices, num_accepted, N, (HV, K, V), "state_pool")
@@ -310,8 +310,8 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
         cu_seqlens = cu_seqlens.contiguous()
     shape = gdn_shape(B, T, H, HV, K, V, N, code)
     _run(dev, (_lib or _load()).gdn_recurrent_steps, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, _r(gates),
-         K ** -0.5 if scale is None else scale, use_qk_l2norm_in_kernel, _r(pool), _p(cu_seqlens), out.data_ptr(),
-         _r(shape))
+         K ** -0.5 if scale is None else scale, use_qk_l2norm_in_kernel, _addr(pool), _p(cu_seqlens), out.data_ptr(),
+         _addr(shape))
     return out
 
 
@@ -417,7 +417,7 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
             raise ValueError(f"conv_state_indices must be int32 [{N}]")
         _, kept = _step_pool(dev, conv_state_pool, conv_state_indices, None, N, (D, W1), "conv_state_pool")
         pool = _b.make_state_pool(conv_state_pool, kept[0], read_initial_state)
-        _run(dev, lib.gdn_conv_fwd_pool, *head, _r(pool), _p(cu), _r(pieces), _r(shape))
+        _run(dev, lib.gdn_conv_fwd_pool, *head, _addr(pool), _p(cu), _addr(pieces), _addr(shape))
         return y, None
     if initial_state is not None:
         if initial_state.shape != (N, D, W1) or initial_state.dtype != x.dtype or initial_state.get_device() != dev:
@@ -431,7 +431,7 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
         final_state = torch.empty_like(initial_state)
     else:
         final_state = x.new_empty((N, D, W1))
-    _run(dev, lib.gdn_conv_fwd, *head, _p(initial_state), _p(cu), _r(pieces), _p(final_state), _r(shape))
+    _run(dev, lib.gdn_conv_fwd, *head, _p(initial_state), _p(cu), _addr(pieces), _p(final_state), _addr(shape))
     return y, final_state
 
 
@@ -462,7 +462,7 @@ def causal_conv1d_update(x, weight, conv_state_pool, conv_state_indices, bias=No
                             "conv_state_pool")
     outs, pieces = _pieces(x, (D,) if split_sizes is None else split_sizes, out, dev, "out")
     _run(dev, (_lib or _load()).gdn_conv_update, rows.data_ptr(), weight.data_ptr(), _p(bias),
-         activation is not None, _r(pool), _p(cu), _r(pieces), _r(shape))
+         activation is not None, _addr(pool), _p(cu), _addr(pieces), _addr(shape))
     if flat:
         outs = [t.squeeze(1) for t in outs]
     return outs[0] if split_sizes is None else tuple(outs)
@@ -488,14 +488,14 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, cu_seqlens=N
             raise ValueError(f"initial_state must be {x.dtype} {list(slot)} on cuda:{dev}")
         initial_state = initial_state.contiguous()
     lib = _lib or _load()
-    need = lib.gdn_conv_bwd_workspace_bytes(_r(shape))
+    need = lib.gdn_conv_bwd_workspace_bytes(_addr(shape))
     ws = _workspace(workspace, need, dev, x)
     dx = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
     dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
     dbias = None if bias is None else torch.empty(D, dtype=torch.float32, device=x.device)
     dinitial = torch.empty(slot, dtype=x.dtype, device=x.device) if output_dinitial else None
     _run(dev, lib.gdn_conv_bwd, rows.data_ptr(), weight.data_ptr(), _p(bias), activation is not None,
-         _p(initial_state), _p(cu), _r(pieces), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dinitial), _r(shape),
+         _p(initial_state), _p(cu), _addr(pieces), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dinitial), _addr(shape),
          ws.data_ptr(), need)
     return dx, dweight, dbias, dinitial
 
@@ -531,24 +531,19 @@ def _gate_rows(x, z, shape):
         return z
     dims, st = z.shape, z.stride()
     D = dims[-1]
-    if st[-1] != 1 and D != 1:
-        return z.contiguous()
-    # the leading dimensions up to `lead` have to be one run of tokens
-    if len(dims) >= 3 and (st[-2] == D or dims[-2] == 1):
-        heads, lead = dims[-2], len(dims) - 3
-    elif len(dims) == 2:
+    if len(dims) == 2:
         heads, lead = 1, 0
+    elif len(dims) > 2 and (st[-2] == D or dims[-2] == 1):
+        heads, lead = dims[-2], len(dims) - 3
     else:
         return z.contiguous()
-    zs = st[lead]
-    run = zs
-    for i in range(lead - 1, -1, -1):
-        run *= dims[i + 1]
-        if dims[i] != 1 and st[i] != run:
+    # the leading dimensions, up to `lead`, have to be one run of tokens
+    zs = run = st[lead]
+    for i in range(lead, 0, -1):
+        run *= dims[i]
+        if st[i - 1] != run:
             return z.contiguous()
-    if dims[lead] == 1 and lead:
-        return z.contiguous()
-    if not heads * D <= zs <= 1 << 31:
+    if st[-1] != 1 or not heads * D <= zs <= 1 << 31:
         return z.contiguous()
     shape.heads, shape.z_stride = heads, zs
     return z
@@ -565,7 +560,7 @@ def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
     x = x.contiguous()
     out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
     _run(dev, (_lib or _load()).gdn_gated_norm, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, out.data_ptr(),
-         _r(shape))
+         _addr(shape))
     return out
 
 
@@ -577,12 +572,12 @@ def fused_gated_rms_norm_bwd(x, z, weight, dy, eps=1e-6, workspace=None):
     z = _gate_rows(x, z, shape)
     x, dy = x.contiguous(), _same(x, dy, "dy")
     lib = _lib or _load()
-    need = lib.gdn_norm_bwd_workspace_bytes(_r(shape))
+    need = lib.gdn_norm_bwd_workspace_bytes(_addr(shape))
     ws = _workspace(workspace, need, dev, x)
     dx, dz = torch.empty_like(x), torch.empty_like(x)
     dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
     _run(dev, lib.gdn_gated_norm_bwd, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, dy.data_ptr(), dx.data_ptr(),
-         dz.data_ptr(), dweight.data_ptr(), _r(shape), ws.data_ptr(), need)
+         dz.data_ptr(), dweight.data_ptr(), _addr(shape), ws.data_ptr(), need)
     return dx, dz, dweight
 
 
@@ -600,7 +595,7 @@ def fused_add_rms_norm(x, residual, weight, eps=1e-6, residual_scale=1.0, weight
     out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
     hidden = torch.empty_like(x) if hidden is None else _given(hidden, x.shape, x, dev, "hidden")
     _run(dev, (_lib or _load()).gdn_add_norm, x.data_ptr(), _p(residual), weight.data_ptr(), residual_scale,
-         weight_offset, eps, out.data_ptr(), hidden.data_ptr(), _r(shape))
+         weight_offset, eps, out.data_ptr(), hidden.data_ptr(), _addr(shape))
     return out, hidden
 
 
@@ -618,11 +613,11 @@ def fused_add_rms_norm_bwd(dy, dhidden, hidden, weight, eps=1e-6, residual_scale
         dhidden = _same(hidden, dhidden, "dhidden")
     hidden = hidden.contiguous()
     lib = _lib or _load()
-    need = lib.gdn_norm_bwd_workspace_bytes(_r(shape))
+    need = lib.gdn_norm_bwd_workspace_bytes(_addr(shape))
     ws = _workspace(workspace, need, dev, hidden)
     dx = torch.empty_like(hidden) if output_dx else None
     dresidual = torch.empty_like(hidden)
     dweight = torch.empty(weight.shape, dtype=torch.float32, device=hidden.device)
     _run(dev, lib.gdn_add_norm_bwd, dy.data_ptr(), _p(dhidden), hidden.data_ptr(), weight.data_ptr(), residual_scale,
-         weight_offset, eps, _p(dx), dresidual.data_ptr(), dweight.data_ptr(), _r(shape), ws.data_ptr(), need)
+         weight_offset, eps, _p(dx), dresidual.data_ptr(), dweight.data_ptr(), _addr(shape), ws.data_ptr(), need)
     return dx, dresidual, dweight

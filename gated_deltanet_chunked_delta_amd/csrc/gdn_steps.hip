@@ -64,15 +64,26 @@ __device__ __forceinline__ float lane_of(float x, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
 }
 
-// Four state elements as fp32, streamed past the caches.
+// Four state elements as fp32.  Stores are streamed past the caches, and so are
+// the loads of a state that is updated in place (256 sequences, HV = 32, fp32: 200
+// against 216 us); where a slot is kept for every token the pass is mostly
+// writes, and plain loads beside them are faster (64 sequences of four tokens,
+// four slots: 118 against 143 us).
 template <typename S> struct Quad;
 template <> struct Quad<float> {
-    static __device__ __forceinline__ f32x4 load(const float *p) { return __builtin_nontemporal_load((const f32x4 *)p); }
+    template <bool STREAM> static __device__ __forceinline__ f32x4 load(const float *p) {
+        if constexpr (STREAM) return __builtin_nontemporal_load((const f32x4 *)p);
+        return *(const f32x4 *)p;
+    }
     static __device__ __forceinline__ void store(float *p, f32x4 x) { __builtin_nontemporal_store(x, (f32x4 *)p); }
 };
 template <> struct Quad<bf16> {
-    static __device__ __forceinline__ f32x4 load(const bf16 *p) {
-        const bf16x4 x = __builtin_nontemporal_load((const bf16x4 *)p);
+    template <bool STREAM> static __device__ __forceinline__ f32x4 load(const bf16 *p) {
+        bf16x4 x;
+        if constexpr (STREAM)
+            x = __builtin_nontemporal_load((const bf16x4 *)p);
+        else
+            x = *(const bf16x4 *)p;
         return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
     }
     static __device__ __forceinline__ void store(bf16 *p, f32x4 x) {
@@ -184,10 +195,19 @@ __global__ void __launch_bounds__(64 * NW) steps_kernel(StepsParams p) {
     f32x4 S[RB][4];
     {
         const SE *src = at(slot);
+        auto read = [&](auto stream) {
 #pragma unroll
-        for (int m = 0; m < RB; ++m)
+            for (int m = 0; m < RB; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[m][e] = Quad<SE>::load(src + (m * 4 * RG + e) * V);
+                for (int e = 0; e < 4; ++e) S[m][e] = Quad<SE>::template load<decltype(stream)::value>(src + (m * 4 * RG + e) * V);
+        };
+        if (sl.cols > 1) {   // the empty statements keep the two kinds of load from being merged into one
+            asm volatile("");
+            read(std::false_type{});
+            asm volatile("");
+        } else {
+            read(std::true_type{});
+        }
     }
     float f = 1.f;                                     // the state is f S
     for (int tc = t0, turn = 0; tc < t1; tc += kTok, turn ^= 1) {
