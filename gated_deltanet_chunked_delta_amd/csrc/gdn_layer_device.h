@@ -21,37 +21,52 @@ typedef float f32x2u __attribute__((ext_vector_type(2), aligned(4)));
 struct f32x8p {
     f32x4 a, b;
 };
+// STREAM: past the caches, for passes over more than they hold.
+template <bool STREAM, typename T> __device__ __forceinline__ T ld(const T *p) {
+    if constexpr (STREAM)
+        return __builtin_nontemporal_load(p);
+    else
+        return *p;
+}
+template <bool STREAM, typename T, typename V> __device__ __forceinline__ void st(T *p, const V &v) {
+    if constexpr (STREAM)
+        __builtin_nontemporal_store((T)v, p);
+    else
+        *p = v;
+}
 template <typename E, int N> struct Raw;
 template <> struct Raw<bf16, 8> {
     typedef bf16x8 T;
-    static __device__ __forceinline__ T load(const bf16 *p) { return *(const bf16x8u *)p; }
-    static __device__ __forceinline__ void store(bf16 *p, const T &r) { *(bf16x8u *)p = r; }
+    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) { return ld<S>((const bf16x8u *)p); }
+    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) { st<S>((bf16x8u *)p, r); }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return (float)r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = (bf16)x; }
 };
 template <> struct Raw<bf16, 4> {
     typedef bf16x4 T;
-    static __device__ __forceinline__ T load(const bf16 *p) { return *(const bf16x4u *)p; }
-    static __device__ __forceinline__ void store(bf16 *p, const T &r) { *(bf16x4u *)p = r; }
+    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) { return ld<S>((const bf16x4u *)p); }
+    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) { st<S>((bf16x4u *)p, r); }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return (float)r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = (bf16)x; }
 };
 template <> struct Raw<float, 4> {
     typedef f32x4 T;
-    static __device__ __forceinline__ T load(const float *p) { return *(const f32x4u *)p; }
-    static __device__ __forceinline__ void store(float *p, const T &r) { *(f32x4u *)p = r; }
+    template <bool S = false> static __device__ __forceinline__ T load(const float *p) { return ld<S>((const f32x4u *)p); }
+    template <bool S = false> static __device__ __forceinline__ void store(float *p, const T &r) { st<S>((f32x4u *)p, r); }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = x; }
 };
 template <> struct Raw<float, 8> {
     typedef f32x8p T;
-    static __device__ __forceinline__ T load(const float *p) { return T{*(const f32x4u *)p, *(const f32x4u *)(p + 4)}; }
-    static __device__ __forceinline__ void store(float *p, const T &r) {
-        *(f32x4u *)p = r.a;
-        *(f32x4u *)(p + 4) = r.b;
+    template <bool S = false> static __device__ __forceinline__ T load(const float *p) {
+        return T{ld<S>((const f32x4u *)p), ld<S>((const f32x4u *)(p + 4))};
+    }
+    template <bool S = false> static __device__ __forceinline__ void store(float *p, const T &r) {
+        st<S>((f32x4u *)p, r.a);
+        st<S>((f32x4u *)(p + 4), r.b);
     }
     static __device__ __forceinline__ T zero() { return T{f32x4{}, f32x4{}}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return e < 4 ? r.a[e] : r.b[e - 4]; }
@@ -75,8 +90,9 @@ template <> struct Two<float> {
 
 // Elements p[0 .. n-1] (n <= N, zeros behind them), and their store: whole, or by
 // fours, twos and one.  tails (uniform): some lane of the wave has 0 < n < N.
-template <typename E, int N = 8> __device__ __forceinline__ typename Raw<E, N>::T load_n(const E *p, int n, bool tails) {
-    if (n >= N) return Raw<E, N>::load(p);
+template <typename E, int N = 8, bool S = false>
+__device__ __forceinline__ typename Raw<E, N>::T load_n(const E *p, int n, bool tails) {
+    if (n >= N) return Raw<E, N>::template load<S>(p);
     if (!tails) return Raw<E, N>::zero();
     E v[N];
 #pragma unroll
@@ -102,10 +118,10 @@ template <typename E, int N = 8> __device__ __forceinline__ typename Raw<E, N>::
     for (int e = 0; e < N; ++e) Raw<E, N>::set(r, e, to_f(v[e]));
     return r;
 }
-template <typename E, int N = 8>
+template <typename E, int N = 8, bool S = false>
 __device__ __forceinline__ void store_n(E *p, const typename Raw<E, N>::T &r, int n, bool tails) {
     if (n >= N) {
-        Raw<E, N>::store(p, r);
+        Raw<E, N>::template store<S>(p, r);
         return;
     }
     if (!tails || n <= 0) return;

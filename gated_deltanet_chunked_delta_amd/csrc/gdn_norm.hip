@@ -43,7 +43,7 @@ template <int L> __device__ __forceinline__ float group_sum(float x, float (*red
     return x;
 }
 
-template <typename E, int L, int NV, bool GATED>
+template <typename E, int L, int NV, bool GATED, bool STREAM>
 __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
     typedef Raw8<E> R;
     typedef typename R::T V;
@@ -76,11 +76,11 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i], tails);
+            xa[i] = load_n<E, 8, GATED && STREAM>(x + at + (i * L + l) * 8, n[i], tails);
             if (GATED)
-                za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i], tails);
+                za[i] = load_n<E, 8, GATED && STREAM>(z + zat + (i * L + l) * 8, n[i], tails);
             else if (res)
-                za[i] = load_n<E>(res + at + (i * L + l) * 8, n[i], tails);
+                za[i] = load_n<E, 8, GATED && STREAM>(res + at + (i * L + l) * 8, n[i], tails);
         }
     };
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
@@ -110,14 +110,14 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                 R::set(o, e, v);
                 if (!GATED) R::set(ho, e, h[i][e]);
             }
-            store_n<E>(y + at + (i * L + l) * 8, o, n[i], tails);
+            store_n<E, 8, STREAM>(y + at + (i * L + l) * 8, o, n[i], tails);
             if (!GATED)
-                if (hid) store_n<E>(hid + at + (i * L + l) * 8, ho, n[i], tails);
+                if (hid) store_n<E, 8, STREAM>(hid + at + (i * L + l) * 8, ho, n[i], tails);
         }
     }
 }
 
-template <typename E, int L, int NV, bool GATED>
+template <typename E, int L, int NV, bool GATED, bool STREAM>
 __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
     typedef Raw8<E> R;
     typedef typename R::T V;
@@ -152,16 +152,19 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E>(x + at + (i * L + l) * 8, n[i], tails);
-            da[i] = load_n<E>(dy + at + (i * L + l) * 8, n[i], tails);
-            if (GATED || z) za[i] = load_n<E>(z + zat + (i * L + l) * 8, n[i], tails);
+            xa[i] = load_n<E, 8, STREAM>(x + at + (i * L + l) * 8, n[i], tails);
+            da[i] = load_n<E, 8, STREAM>(dy + at + (i * L + l) * 8, n[i], tails);
+            if (GATED || z) za[i] = load_n<E, 8, STREAM>(z + zat + (i * L + l) * 8, n[i], tails);
         }
     };
+    // the longest rows have no registers left for the next row's loads (128 a thread)
+    constexpr bool AHEAD = L * NV <= 1024;
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
-    if (row < p.rows) load(row);
+    if (AHEAD && row < p.rows) load(row);
     for (int turn = 0; row < p.rows; row += groups, turn ^= 1) {
         float h[NV][8], u[NV][8], g[NV][8];
         float ss = 0.f, sh = 0.f;
+        if (!AHEAD) load(row);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                 const float t = GATED ? u[i][e] * w[i][e] * (g[i][e] * sigmoid_f(g[i][e])) : u[i][e] * w[i][e];
                 sh = fmaf(t, h[i][e], sh);
             }
-        if (row + groups < p.rows) load(row + groups);
+        if (AHEAD && row + groups < p.rows) load(row + groups);
         const float r = rsqrtf(group_sum<L>(ss, red, turn) * inv + p.eps);
         const float c = group_sum<L>(sh, red2, turn) * r * inv;       // mean(n u)
         const int64_t at = row * D;
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                     R::set(o, e, p.alpha * d);
                 }
             }
-            if (GATED || dx) store_n<E>(dx + at + (i * L + l) * 8, o, n[i], tails);
-            if (GATED || dz) store_n<E>(dz + at + (i * L + l) * 8, oz, n[i], tails);
+            if (GATED || dx) store_n<E, 8, STREAM>(dx + at + (i * L + l) * 8, o, n[i], tails);
+            if (GATED || dz) store_n<E, 8, STREAM>(dz + at + (i * L + l) * 8, oz, n[i], tails);
         }
     }
     // the workgroup's sums of dw: over its groups in order
@@ -287,12 +290,27 @@ int norm_bwd_blocks(int64_t rows, int D) {
     return (int)(b < most ? b : most);
 }
 
+// Passes over more than the 256 MiB of the last cache are streamed past it: 16,384
+// rows of 5120 forward 120 against 125 us (stores only: streamed loads too, 123),
+// 4096 backward 127 against 135; 16,384 x 32 gated rows of 128 forward 75 against
+// 83, backward 126 against 133.  Smaller outputs stay there for their reader.
+bool streams(const NormParams &p, size_t elem, int tensors) { return (size_t)p.rows * p.D * elem * tensors > (256u << 20); }
+
 template <typename E, int L, int NV, bool GATED>
 void launch_cfg(const NormParams &p, bool bwd, hipStream_t st) {
-    if (bwd)
-        norm_bwd_kernel<E, L, NV, GATED><<<norm_bwd_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p);
-    else
-        norm_kernel<E, L, NV, GATED><<<norm_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p);
+    if (bwd) {
+        const int grid = norm_bwd_blocks(p.rows, p.D);
+        if (streams(p, sizeof(E), 5))
+            norm_bwd_kernel<E, L, NV, GATED, true><<<grid, threads_of(L), 0, st>>>(p);
+        else
+            norm_bwd_kernel<E, L, NV, GATED, false><<<grid, threads_of(L), 0, st>>>(p);
+    } else {
+        const int grid = norm_blocks(p.rows, p.D);
+        if (streams(p, sizeof(E), GATED ? 3 : 4))
+            norm_kernel<E, L, NV, GATED, true><<<grid, threads_of(L), 0, st>>>(p);
+        else
+            norm_kernel<E, L, NV, GATED, false><<<grid, threads_of(L), 0, st>>>(p);
+    }
 }
 
 template <typename E, bool GATED>
