@@ -21,40 +21,58 @@ typedef float f32x2u __attribute__((ext_vector_type(2), aligned(4)));
 struct f32x8p {
     f32x4 a, b;
 };
-// STREAM: past the caches, for passes over more than they hold.
-template <bool STREAM, typename T> __device__ __forceinline__ T ld(const T *p) {
-    if constexpr (STREAM)
-        return __builtin_nontemporal_load(p);
-    else
-        return *p;
-}
-template <bool STREAM, typename T, typename V> __device__ __forceinline__ void st(T *p, const V &v) {
-    if constexpr (STREAM)
-        __builtin_nontemporal_store((T)v, p);
-    else
-        *p = v;
-}
+// S: past the caches, for passes over more than they hold.
 template <typename E, int N> struct Raw;
 template <> struct Raw<bf16, 8> {
     typedef bf16x8 T;
-    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) { return ld<S>((const bf16x8u *)p); }
-    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) { st<S>((bf16x8u *)p, r); }
+    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) {
+        if constexpr (S)
+            return __builtin_nontemporal_load((const bf16x8u *)p);
+        else
+            return *(const bf16x8u *)p;
+    }
+    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) {
+        if constexpr (S)
+            __builtin_nontemporal_store(r, (bf16x8u *)p);
+        else
+            *(bf16x8u *)p = r;
+    }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return (float)r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = (bf16)x; }
 };
 template <> struct Raw<bf16, 4> {
     typedef bf16x4 T;
-    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) { return ld<S>((const bf16x4u *)p); }
-    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) { st<S>((bf16x4u *)p, r); }
+    template <bool S = false> static __device__ __forceinline__ T load(const bf16 *p) {
+        if constexpr (S)
+            return __builtin_nontemporal_load((const bf16x4u *)p);
+        else
+            return *(const bf16x4u *)p;
+    }
+    template <bool S = false> static __device__ __forceinline__ void store(bf16 *p, const T &r) {
+        if constexpr (S)
+            __builtin_nontemporal_store(r, (bf16x4u *)p);
+        else
+            *(bf16x4u *)p = r;
+    }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return (float)r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = (bf16)x; }
 };
 template <> struct Raw<float, 4> {
     typedef f32x4 T;
-    template <bool S = false> static __device__ __forceinline__ T load(const float *p) { return ld<S>((const f32x4u *)p); }
-    template <bool S = false> static __device__ __forceinline__ void store(float *p, const T &r) { st<S>((f32x4u *)p, r); }
+    template <bool S = false> static __device__ __forceinline__ T load(const float *p) {
+        if constexpr (S)
+            return __builtin_nontemporal_load((const f32x4u *)p);
+        else
+            return *(const f32x4u *)p;
+    }
+    template <bool S = false> static __device__ __forceinline__ void store(float *p, const T &r) {
+        if constexpr (S)
+            __builtin_nontemporal_store(r, (f32x4u *)p);
+        else
+            *(f32x4u *)p = r;
+    }
     static __device__ __forceinline__ T zero() { return T{}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return r[e]; }
     static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = x; }
@@ -62,11 +80,11 @@ template <> struct Raw<float, 4> {
 template <> struct Raw<float, 8> {
     typedef f32x8p T;
     template <bool S = false> static __device__ __forceinline__ T load(const float *p) {
-        return T{ld<S>((const f32x4u *)p), ld<S>((const f32x4u *)(p + 4))};
+        return T{Raw<float, 4>::load<S>(p), Raw<float, 4>::load<S>(p + 4)};
     }
     template <bool S = false> static __device__ __forceinline__ void store(float *p, const T &r) {
-        st<S>((f32x4u *)p, r.a);
-        st<S>((f32x4u *)(p + 4), r.b);
+        Raw<float, 4>::store<S>(p, r.a);
+        Raw<float, 4>::store<S>(p + 4, r.b);
     }
     static __device__ __forceinline__ T zero() { return T{f32x4{}, f32x4{}}; }
     static __device__ __forceinline__ float get(const T &r, int e) { return e < 4 ? r.a[e] : r.b[e - 4]; }

@@ -278,22 +278,27 @@ Split split_of(int D) {
     return {1024, 2};
 }
 
-int norm_blocks(int64_t rows, int D) {
-    const int L = split_of(D).L, gpb = threads_of(L) / L;
-    const int64_t b = (rows + gpb - 1) / gpb;
-    return (int)(b < 2048 ? b : 2048);
-}
-// Fewer workgroups than in the forward pass: each leaves a row of partial sums.
-int norm_bwd_blocks(int64_t rows, int D) {
-    const int L = split_of(D).L, gpb = threads_of(L) / L;
-    const int64_t b = (rows + gpb - 1) / gpb, most = L <= 64 ? 1024 : 512;
+// Workgroups of `waves` waves in all, fewer for few rows.
+int blocks_of(int64_t rows, int D, int waves) {
+    const int L = split_of(D).L, t = threads_of(L), gpb = t / L;
+    const int64_t b = (rows + gpb - 1) / gpb, most = waves * 64 / t;
     return (int)(b < most ? b : most);
 }
+// Forward: many short-lived waves (16,384 x 32 gated rows of 128: 32768 waves 68
+// us, 8192 74), but few of the 1024-thread workgroups (8192 rows of 8192: 4096
+// waves 94 us, 8192 97, 32768 100).
+int norm_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L == 1024 ? 4096 : 32768); }
+// Backward: two waves a SIMD, walking the rows with the next one loading, keep the
+// memory busiest and leave the fewest partial sums (16,383 rows of 4096: 2048
+// waves 114 us, 4096 125, 1024 157; gated rows of 128 111, 125 and 135), and every
+// CU has a workgroup.
+int norm_bwd_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L == 1024 ? 4096 : 2048); }
 
 // Passes over more than the 256 MiB of the last cache are streamed past it: 16,384
 // rows of 5120 forward 120 against 125 us (stores only: streamed loads too, 123),
 // 4096 backward 127 against 135; 16,384 x 32 gated rows of 128 forward 75 against
-// 83, backward 126 against 133.  Smaller outputs stay there for their reader.
+// 83, backward 126 against 133 (before the grids above).  Smaller outputs stay
+// there for their reader.
 bool streams(const NormParams &p, size_t elem, int tensors) { return (size_t)p.rows * p.D * elem * tensors > (256u << 20); }
 
 template <typename E, int L, int NV, bool GATED>

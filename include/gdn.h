@@ -598,7 +598,7 @@ int gdn_add_norm(const void *x, const void *residual, const void *weight,
                  void *out, void *hidden, const gdn_norm_shape *shape, void *stream);
 
 /* Bytes of device workspace of the two backward passes below: one row of D
- * floats per workgroup (at most 1024); 0 for invalid sizes or without rows. */
+ * floats per workgroup (at most 512); 0 for invalid sizes or without rows. */
 size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape *shape);
 
 /* Backward pass of gdn_gated_norm.  With n = x r and u = dout weight silu(z):

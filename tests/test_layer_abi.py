@@ -194,7 +194,7 @@ def test_norm_workspace_size():
     assert size(rows=0) == 0 and size(rows=-1) == 0 and size(D=0) == 0 and size(D=16385) == 0
     for rows, D in ((1, 128), (1000, 128), (1 << 20, 64), (1 << 20, 4096)):
         n, rest = divmod(size(rows=rows, D=D), 4 * D)
-        assert rest == 0 and 1 <= n <= min(rows, 1024)
+        assert rest == 0 and 1 <= n <= min(rows, 512)
 
 
 # ---------------------------------------------------------------------------
