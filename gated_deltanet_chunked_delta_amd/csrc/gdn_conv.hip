@@ -558,16 +558,20 @@ int lane_blocks(const ConvParams &p, int C) {
     return (int)((v + 63) / 64);
 }
 constexpr int kStripWaves = 4096;
-// Tokens of a strip: whole load batches, long enough that the W-1 rows read
-// twice are few, short enough for 4096 waves.
+// Tokens of a strip: whole load batches; 12 or 16 forward and 48 or 64 backward
+// (W = 4: 16,384 tokens of 3392 columns and 5036 a sequence forward 159 us, with
+// 24 163, with 6 172; the gradients of 16,384 tokens of 8192 columns 173, with 96
+// 180, with 24 182: longer ones leave a CU's rows far apart, shorter ones read
+// more rows twice and leave more partial sums), fewer where that leaves less than
+// 4096 waves.
 int strip_len(int64_t T_tot, int64_t D, int C, int lo, int hi) {
     int L = hi;
     while (L > lo && ((T_tot + L - 1) / L) * col_blocks(D, C) < kStripWaves) L >>= 1;
     return L;
 }
-int fwd_strip(int64_t T_tot, int64_t D, int W) { return strip_len(T_tot, D, 8, batch_rows(W), 8 * batch_rows(W)); }
+int fwd_strip(int64_t T_tot, int64_t D, int W) { return strip_len(T_tot, D, 8, batch_rows(W), 4 * batch_rows(W)); }
 int bwd_strip(int64_t T_tot, int64_t D, int W) {
-    return strip_len(T_tot, D, kBwdCols, batch_rows(W), 32 * batch_rows(W));
+    return strip_len(T_tot, D, kBwdCols, batch_rows(W), 16 * batch_rows(W));
 }
 int bwd_groups(int64_t T_tot, int64_t D, int W) {
     const int64_t L = bwd_strip(T_tot, D, W), strips = (T_tot + L - 1) / L;
@@ -626,7 +630,7 @@ template <typename F> void for_width(int W, F f) {
 
 int64_t conv_grid(int64_t T_tot, int64_t D, int64_t N, int W) {
     const int64_t L = fwd_strip(T_tot, D, W), cb = col_blocks(D + 16, 8);   // three pieces: at most two vectors more
-    return ((T_tot + L - 1) / L + 3) / 4 * cb + (N * cb + 3) / 4;
+    return ((T_tot + L - 1) / L + 3) / 4 * cb + (N * cb * 2 + 3) / 4;   // lanes of four columns by sequence
 }
 
 hipError_t launch_conv(const ConvParams &p, int dtype, hipStream_t stream, Profiler *prof) {

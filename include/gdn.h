@@ -508,7 +508,7 @@ typedef struct gdn_conv_pieces {
  * Tensors are aligned to their element.  Arithmetic is fp32, rounded once.  No
  * workspace.  Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a
  * sequence, more than 2^31 - 65 of them, or too many for one launch: 2^24 - 1
- * blocks of 128 tokens by 512 columns), GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED,
+ * blocks of 48 tokens by 512 columns), GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED,
  * GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
 int gdn_conv_fwd(const void *x, const void *weight, const void *bias, int silu,
                  const void *initial_state, const int32_t *cu_seqlens,
@@ -532,7 +532,7 @@ int gdn_conv_update(const void *x, const void *weight, const void *bias, int sil
                     const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream);
 
 /* Bytes of device workspace gdn_conv_bwd needs: W + 1 floats per column for
- * each block of 12 to 512 tokens (the more tokens and columns, the longer); 0
+ * each block of 12 to 256 tokens (the more tokens and columns, the longer); 0
  * for invalid sizes or without tokens. */
 size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape);
 

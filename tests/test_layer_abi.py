@@ -130,10 +130,10 @@ def test_conv_refusals_of_one_entry(entry, kw, want):
 def test_conv_workspace_size():
     size = lambda **kw: gdn.gdn_conv_bwd_workspace_bytes(gdn.gdn_conv_shape(**{**CONV_SHAPE, **kw}))
     assert size(T=0) == 0 and size(W=5) == 0 and size(D=0) == 0 and size(B=-1) == 0
-    # W + 1 floats a column for each block of 12 to 512 tokens
+    # W + 1 floats a column for each block of 12 to 256 tokens
     for B, T, D, W in ((1, 1, 32, 4), (2, 5, 33, 2), (4, 4096, 8192, 4), (1, 70000, 64, 3)):
         rows, rest = divmod(size(B=B, T=T, D=D, W=W), 4 * D * (W + 1))
-        assert rest == 0 and -(-B * T // 512) <= rows <= -(-B * T // 12)
+        assert rest == 0 and -(-B * T // 256) <= rows <= -(-B * T // 12)
 
 
 # ---------------------------------------------------------------------------
