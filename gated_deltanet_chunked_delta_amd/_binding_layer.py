@@ -8,6 +8,9 @@ instead of ctypes objects, one struct a call, messages built only when they are
 raised, torch's raw stream handle (0.1 us; ``current_stream`` takes 1.9).  A
 call on another device than the current one makes that device current for its
 duration.
+
+With ``cu_seqlens[N] < T`` (a batch padded to a fixed T) the rows behind the last
+sequence are neither read nor written: in a new output tensor they are undefined.
 """
 from __future__ import annotations
 

@@ -352,7 +352,7 @@ gdn::StepSlots slots_of(const gdn_step_pool &pl) {
 int check_conv(const gdn_conv_shape *shape, const gdn_conv_pieces *pieces, const int32_t *cu_seqlens) {
     if (!shape) return GDN_ERR_NULL;
     const gdn_conv_shape &s = *shape;
-    if (s.B < 0 || s.T < 0 || s.N < 0 || s.D <= 0) return GDN_ERR_SHAPE;
+    if (s.B < 0 || s.T < 0 || s.N < 0 || s.D <= 0 || s.D > (1 << 26)) return GDN_ERR_SHAPE;
     if (gdn::elem_bytes(s.dtype) == 0 || gdn::elem_bytes(s.weight_dtype) == 0) return GDN_ERR_DTYPE;
     if (s.W < 2 || s.W > 4) return GDN_ERR_UNSUPPORTED;
     if (s.weight_dtype != s.dtype && s.weight_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
@@ -705,7 +705,7 @@ int gdn_conv_update(const void *x, const void *weight, const void *bias, int sil
 }
 
 size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape) {
-    if (!shape || shape->B < 0 || shape->T < 0 || shape->D <= 0 || shape->W < 2 || shape->W > 4) return 0;
+    if (!shape || shape->B < 0 || shape->T < 0 || shape->D <= 0 || shape->D > (1 << 26) || shape->W < 2 || shape->W > 4) return 0;
     const int64_t tokens = (int64_t)shape->B * shape->T;
     return tokens > INT_MAX - 64 ? 0 : gdn::conv_bwd_workspace_bytes(tokens, shape->D, shape->W);
 }

@@ -190,6 +190,11 @@ template <int U, typename V> __device__ __forceinline__ V pick(const V *v, int i
     return __builtin_bit_cast(V, r);
 }
 
+// Tokens of all sequences: rows behind them are neither read nor written.
+__device__ __forceinline__ int tokens_of(const ConvParams &p) {
+    return p.cu_seqlens ? cu_at(p.cu_seqlens, p.N, p.T_tot) : p.T_tot;
+}
+
 // The sequences as a strip walks them.
 struct Walk {
     int seq, t0, t1;     // t0 <= the current token < t1
@@ -257,7 +262,8 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvParams p, int L, int nstr
     const Lane<E, C> ln(p, (blk % cblocks) * 64 + lane);
     const int n = ln.n;
     if (strip >= nstrips) return;
-    const int s0 = strip * L, s1 = min(s0 + L, p.T_tot);
+    const int s0 = strip * L, s1 = min(s0 + L, tokens_of(p));
+    if (s0 >= s1) return;
     const E *__restrict__ x = (const E *)p.x;
     V xa[U], before[W - 1];
     // rows of one batch, up to the strip's end whatever sequence they belong to
@@ -443,8 +449,9 @@ conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
     for (int j = 0; j <= W; ++j)
 #pragma unroll
         for (int e = 0; e < C; ++e) dw[j][e] = 0.f;
-    if (strip < nstrips) {
-        const int s0 = strip * L, s1 = min(s0 + L, p.T_tot), se = min(s1 + W - 1, p.T_tot);
+    const int end = tokens_of(p);
+    if (strip < nstrips && strip * L < end) {
+        const int s0 = strip * L, s1 = min(s0 + L, end), se = min(s1 + W - 1, end);
         const E *__restrict__ x = (const E *)p.x;
         E *__restrict__ dx = (E *)p.dx;
         V xa[U], da[U], before[W - 1];

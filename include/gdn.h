@@ -411,7 +411,13 @@ int gdn_chunk_bwd(const void *q, const void *k, const void *v,
                   const gdn_shape *shape, void *workspace, size_t workspace_bytes,
                   void *stream);
 
-/* Slots of a pool that a step of a few tokens per sequence reads and writes: a
+/* The operators around the delta rule.  Beyond the conventions above: with
+ * cu_seqlens[N] < T (a batch padded to a fixed T, as a captured graph has it) the
+ * rows of tokens behind the last sequence are neither read nor written.  Two
+ * calls that may run at the same time need workspaces of their own; calls in
+ * order on one stream may share one.
+ *
+ * Slots of a pool that a step of a few tokens per sequence reads and writes: a
  * token and its drafts, verified in one call.  The states (gdn_recurrent_steps)
  * or convolution histories (gdn_conv_update) of the running sequences lie in
  * `pool_size` slots; sequence n has `cols` of them, indices[n, 0 .. cols-1].
@@ -467,7 +473,8 @@ int gdn_recurrent_steps(const void *q, const void *k, const void *v,
 
 /* Sizes of the short convolution.
  *   B, T, N       as in gdn_shape (with cu_seqlens B = 1)
- *   D, W          columns, and the width: 2, 3 or 4 (GDN_ERR_UNSUPPORTED)
+ *   D, W          columns, at most 2^26, and the width: 2, 3 or 4
+ *                 (GDN_ERR_UNSUPPORTED)
  *   dtype         gdn_dtype of x, the outputs and the histories
  *   weight_dtype  of weight and bias: dtype or GDN_F32
  *   x_stride      elements between the rows of x, at least D (x may be a part

@@ -93,6 +93,8 @@ STEPS = {   # H, HV, K, V, lengths (an int: equal), columns, raw gates, pool typ
     "long": (1, 2, 64, 128, [70, 1], 2, True, F32, True),
     "no_norm": (1, 2, 64, 64, [5, 2, 4], 1, False, BF, False),
     "heads": (4, 4, 64, 64, (2,) * 33, 2, True, F32, True),
+    # more columns than lanes, slots behind the 64th read and written
+    "many_columns": (1, 1, 64, 64, (69,) * 4, 70, False, F32, True),
     # 256 heads and more, 2048 and more: wider column splits
     "many_heads": (2, 8, 128, 128, [i % 5 for i in range(35)], 2, True, F32, True),
     "many_heads_bf16": (8, 8, 64, 128, (10,) * 33, 1, False, BF, True),
@@ -402,6 +404,69 @@ def test_add_norm_and_backward(rows, D, dtype):
     grads = layer.add_norm_bwd(dy, None, hid, w, weight_offset=1.0)
     assert none is None and torch.equal(dw, got[2])
     _near("dresidual alone", dres, *grads["dresidual"], 128)
+
+
+def test_inputs_off_alignment():
+    """Contiguous tensors that begin one element into their storage: every
+    operator takes them and gives the bits of the aligned call."""
+    gdn = _gdn()
+
+    def off(t):
+        if t is None or t.dtype not in (BF, F32):
+            return t
+        u = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view(t.shape)
+        return u.copy_(t)
+    for dtype in (BF, F32):
+        x = {k: None if t is None else t.to(DEV) for k, t in _steps_inputs("verify", dtype).items()}
+        g, beta = x["g"].float(), x["beta"].float()
+        outs = []
+        for f in (lambda t: t, off):
+            pool = x["pool"].clone()
+            o = gdn.fused_recurrent_gated_delta_rule_steps(f(x["q"]), f(x["k"]), f(x["v"]), f(g), f(beta), pool, x["idx"],
+                                                           num_accepted=x["acc"], use_qk_l2norm_in_kernel=True,
+                                                           out=f(torch.empty_like(x["v"])))
+            outs.append((o, pool))
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        c = _conv_inputs("packed", dtype)
+        xs = c["x"].contiguous()
+        for call in (lambda f: gdn.causal_conv1d(f(xs), f(c["w"]), f(c["b"]), initial_state=f(c["h0"]), cu_seqlens=c["cu"]),
+                     lambda f: gdn.causal_conv1d_bwd(f(xs), f(c["w"]), f(c["dy"]), f(c["b"]), initial_state=f(c["h0"]),
+                                                     cu_seqlens=c["cu"], output_dinitial=True),
+                     lambda f: gdn.fused_gated_rms_norm_bwd(f(xs), f(c["dy"]), f(c["w"][:, 0].contiguous()), f(c["dy"])),
+                     lambda f: gdn.fused_add_rms_norm(f(xs), f(c["dy"]), f(c["w"][:, 0].contiguous()))):
+            assert all(torch.equal(a, b) for a, b in zip(call(lambda t: t), call(off)))
+
+
+def test_rows_behind_the_last_sequence():
+    """A packed batch padded to a fixed T: the rows behind the last sequence stay
+    as they were, the others and the weights' gradients are the unpadded call's."""
+    gdn = _gdn()
+    x = _conv_inputs("packed", BF)
+    T, D, pad = x["x"].shape[1], x["x"].shape[2], 41
+    more = x["draw"].randn(1, pad, D, dtype=BF).to(DEV).fill_(float("nan"))
+    wide, dy = torch.cat([x["x"], more], 1), torch.cat([x["dy"], more], 1)
+    out = torch.full_like(wide, 7)
+    y, fin = gdn.causal_conv1d(wide, x["w"], x["b"], initial_state=x["h0"], cu_seqlens=x["cu"], out=out)
+    want, wfin = gdn.causal_conv1d(x["x"], x["w"], x["b"], initial_state=x["h0"], cu_seqlens=x["cu"])
+    assert y is out and torch.equal(y[:, :T], want) and torch.equal(fin, wfin) and (y[:, T:] == 7).all()
+    got = gdn.causal_conv1d_bwd(wide, x["w"], dy, x["b"], initial_state=x["h0"], cu_seqlens=x["cu"], output_dinitial=True)
+    ref = layer.conv_bwd(x["x"], x["w"], x["dy"], x["b"], x["h0"], x["cu"])
+    _near("dx", got[0][:, :T], *ref["dx"], 16)
+    _near("dweight", got[1], *ref["dweight"], 128)
+    _near("dbias", got[2], *ref["dbias"], 128)
+    _near("dinitial", got[3], *ref["dinitial"], 16)
+    s = {k: None if t is None else t.to(DEV) for k, t in _steps_inputs("ragged_bf16", BF).items()}
+    n = s["v"].shape[1]
+    outs = []
+    for extra in (0, 9):
+        q, k, v, a, b = (torch.cat([s[i], torch.full_like(s[i][:, :1], float("nan")).expand(-1, extra, *s[i].shape[2:])], 1)
+                         for i in ("q", "k", "v", "a", "b"))
+        pool, out = s["pool"].clone(), torch.full_like(v, 7)
+        gdn.fused_recurrent_gated_delta_rule_steps(q, k, v, None, None, pool, s["idx"], cu_seqlens=s["cu"], num_accepted=s["acc"],
+                                                   A_log=s["A_log"], dt_bias=s["dt_bias"], a_raw=a, b_raw=b, out=out)
+        outs.append((out[:, :n], pool))
+        assert (out[:, n:] == 7).all()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
 
 
 def test_norm_without_rows():

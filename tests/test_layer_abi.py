@@ -98,6 +98,7 @@ def _conv(entry, shape=None, pieces=None, cu=None, no_shape=False, pool=None, no
     (dict(shape=dict(T=-1)), -2), (dict(shape=dict(N=3)), -2), (dict(cu=FAKE), -2), (dict(shape=dict(D=0)), -2),
     (dict(shape=dict(B=1, N=0), cu=FAKE), -2), (dict(shape=dict(B=1 << 16, N=1 << 16, T=1 << 16)), -2),
     (dict(shape=dict(x_stride=31)), -2), (dict(shape=dict(x_stride=(1 << 31) + 1)), -2),
+    (dict(shape=dict(D=(1 << 26) + 1, x_stride=1 << 27)), -2),
     (dict(shape=dict(B=1, T=1 << 28, N=1, D=1 << 14, x_stride=1 << 14), pieces=_pieces((1 << 14, 0, 0))), -2),   # grid
     (dict(shape=dict(dtype=4)), -3), (dict(shape=dict(weight_dtype=-1)), -3),
     (dict(shape=dict(W=1)), -4), (dict(shape=dict(W=5)), -4), (dict(shape=dict(dtype=F32)), -4),   # bf16 weights of fp32 x
