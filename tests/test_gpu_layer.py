@@ -439,6 +439,69 @@ def test_inputs_off_alignment():
             assert all(torch.equal(a, b) for a, b in zip(call(lambda t: t), call(off)))
 
 
+def test_padding_rows_and_foreign_slots_do_not_leak():
+    """NaN in the inputs of padding rows and in slots that no row names change
+    nothing; a slot named for every column of a row ends with its last state."""
+    gdn = _gdn()
+    x = {k: None if t is None else t.to(DEV) for k, t in _steps_inputs("verify", BF).items()}
+    x["idx"][2] = x["idx"][2, 1]
+    named = set(i for i in x["idx"].flatten().tolist() if i >= 0)
+    foreign = [i for i in range(x["pool"].shape[0]) if i not in named]
+    outs = []
+    for bad in (False, True):
+        q, k, v, a, b, pool = (x[n].clone() for n in ("q", "k", "v", "a", "b", "pool"))
+        if bad:
+            for t in (q, k, v, a, b):
+                t[1] = float("nan")                       # row 1 is padding
+            pool[foreign] = float("nan")
+        o = gdn.fused_recurrent_gated_delta_rule_steps(q, k, v, None, None, pool, x["idx"], num_accepted=x["acc"],
+                                                       use_qk_l2norm_in_kernel=True, A_log=x["A_log"],
+                                                       dt_bias=x["dt_bias"], a_raw=a, b_raw=b)
+        outs.append((o, pool[sorted(named)]))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and not outs[0][0][1].any()
+    one = x["pool"].clone()
+    gdn.fused_recurrent_gated_delta_rule_steps(x["q"], x["k"], x["v"], None, None, one, x["idx"][:, 1].contiguous(),
+                                               use_qk_l2norm_in_kernel=True, A_log=x["A_log"], dt_bias=x["dt_bias"],
+                                               a_raw=x["a"], b_raw=x["b"])
+    slot = int(x["idx"][2, 1])
+    assert torch.equal(outs[0][1][sorted(named).index(slot)], one[slot])
+    d = Draw(6)
+    xs, w, pool = d.randn(4, 3, 40, dtype=BF).to(DEV), d.randn(40, 4, dtype=BF).to(DEV), d.randn(9, 40, 3, dtype=BF).to(DEV)
+    idx = torch.tensor([[1, 2, 3], [-1, 4, 4], [6, 6, 6], [5, 9, 7]], dtype=torch.int32, device=DEV)
+    ref, after, mag = layer.conv_update(xs, w, pool, idx)
+    xs[1] = float("nan")
+    pool[0] = pool[8] = float("nan")
+    y = gdn.causal_conv1d_update(xs, w, pool, idx)
+    _near("y", y, ref, mag, 8)
+    assert (_np(pool[1:8]) == after[1:8]).all()
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams at once, each call with its own outputs
+    and workspace, give what they give alone."""
+    gdn = _gdn()
+    x = _conv_inputs("split_slice", BF)
+    d = Draw(8)
+    h, dy = d.randn(3000, 1024, dtype=BF).to(DEV), d.randn(3000, 1024, dtype=BF).to(DEV)
+    w = d.randn(1024, dtype=BF).to(DEV)
+    dys = [t.contiguous() for t in x["dy"].split(x["split"], -1)]
+
+    def step():
+        return [*gdn.fused_add_rms_norm_bwd(dy, None, h, w), *gdn.fused_gated_rms_norm_bwd(h, dy, w, dy),
+                *(t for t in gdn.causal_conv1d_bwd(x["x"], x["w"], dys, x["b"], initial_state=x["h0"]) if t is not None)]
+    alone = step()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step()
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, alone))
+
+
 def test_rows_behind_the_last_sequence():
     """A packed batch padded to a fixed T: the rows behind the last sequence stay
     as they were, the others and the weights' gradients are the unpadded call's."""
