@@ -208,6 +208,8 @@ def _step_pool(dev, data, indices, num_accepted, N, slot, name):
         raise ValueError(f"{name} must be a contiguous [P,{','.join(map(str, slot))}]")
     if indices.dtype != torch.int32 or not 1 <= len(dims) <= 2 or dims[0] != N or dims[-1] == 0 < N:
         raise ValueError(f"{name}'s indices must be int32 [{N}] or [{N},cols]")
+    if (data.shape[0] | dims[-1]) >> 31:   # sizes are 32-bit in the structs, which do not check them
+        raise ValueError(f"{name}: fewer than 2^31 slots and columns are wanted")
     if num_accepted is not None:
         if num_accepted.dtype != torch.int32 or num_accepted.shape != (N,):
             raise ValueError(f"num_accepted must be int32 [{N}]")
@@ -233,6 +235,8 @@ def _sequences(dev, B, cu_seqlens):
         raise ValueError("cu_seqlens must be int32 [N+1]")
     if cu_seqlens.get_device() != dev:
         raise ValueError(f"cu_seqlens must be on cuda:{dev}")
+    if cu_seqlens.shape[0] >> 31:
+        raise ValueError("cu_seqlens must have fewer than 2^31 entries")
     return cu_seqlens.shape[0] - 1
 
 
@@ -281,6 +285,8 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
         raise ValueError("q, k, v must share one dtype (bfloat16 or float32)")
     B, T, H, K = dims
     HV, V = vdims[2], vdims[3]
+    if (B | T) >> 31:
+        raise ValueError("q must be [B,T,H,K] with sizes below 2^31")
     N = _sequences(dev, B, cu_seqlens)
     gates = gp = bp = None
     if g is None and beta is None:
@@ -341,6 +347,8 @@ def _conv_args(x, weight, bias, cu_seqlens, activation):
         raise ValueError("x must be [B,T,D]")
     dev, code = _gpu(x, "x")
     B, T, D = dims
+    if (B | T | D) >> 31:
+        raise ValueError("x must be [B,T,D] with sizes below 2^31")
     if weight.dim() != 2 or weight.shape[0] != D:
         raise ValueError(f"weight must be [{D},W]")
     if bias is not None:
@@ -510,8 +518,8 @@ def _norm_args(x, weight):
     """x's device number, the sizes of its rows, and weight, contiguous."""
     dev, code = _gpu(x, "x")
     D = x.shape[-1] if x.dim() else 0
-    if D == 0 or weight.shape != (D,):
-        raise ValueError(f"x must be [...,D] and weight [D], D > 0 (x {list(x.shape)}, weight {list(weight.shape)})")
+    if not 0 < D < 1 << 31 or weight.shape != (D,):
+        raise ValueError(f"x must be [...,D] and weight [D], 0 < D < 2^31 (x {list(x.shape)}, weight {list(weight.shape)})")
     wcode = code if weight.dtype == x.dtype else _weight(x, weight)
     if weight.get_device() != dev:
         raise ValueError(f"weight must be on cuda:{dev}")
