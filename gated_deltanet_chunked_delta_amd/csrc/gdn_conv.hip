@@ -587,8 +587,8 @@ int bwd_groups(int64_t T_tot, int64_t D, int W) {
 
 // Passes over more than the 256 MiB of the last cache are streamed past it (the
 // forward pass its outputs only: the strips share rows of x): 62,386 packed
-// tokens of 8192 columns 444 against 455 us, the gradients of 16,384 tokens 181
-// against 187.
+// tokens of 8192 columns 437 against 459 us, the gradients of 16,384 tokens 175
+// against 182.
 bool streams(const ConvParams &p, size_t elem, int tensors) {
     return (size_t)p.T_tot * p.D * elem * tensors > (256u << 20);
 }

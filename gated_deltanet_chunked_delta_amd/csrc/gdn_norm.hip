@@ -43,6 +43,40 @@ template <int L> __device__ __forceinline__ float group_sum(float x, float (*red
     return x;
 }
 
+// Elements [at, at + n) of a row: a lane's vector.  The last one of a row of an
+// odd length ends with the row and begins `dup` elements inside its neighbour's,
+// so that every access is a whole vector (rows of fewer than eight elements
+// aside): both lanes compute and store the same values there, after the whole row
+// has been read, and the sums leave them to the neighbour (131,072 gated rows of
+// 187 with the last elements by fours, twos and one instead: 49 against 31 us,
+// their gradients 146 against 62; 9000 rows of 5001 117 against 81).
+struct Part {
+    int at, n, dup;
+    Part() = default;
+    __device__ __forceinline__ Part(int D, int v) {
+        const int left = D - v * 8;
+        dup = left > 0 && left < 8 && D >= 8 ? 8 - left : 0;
+        at = v * 8 - dup;
+        n = min(max(D - at, 0), 8);
+    }
+};
+// Sum of a b over the lane's own elements.
+template <int NV> __device__ __forceinline__ float sum_own(const float (*a)[8], const float (*b)[8], const Part *pt, bool odd) {
+    float s = 0.f;
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(e >= pt[i].dup ? a[i][e] : 0.f, b[i][e], s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(a[i][e], b[i][e], s);
+    }
+    return s;
+}
+
 template <typename E, int L, int NV, bool GATED, bool STREAM>
 __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
     typedef Raw8<E> R;
@@ -57,13 +91,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
     E *hid = (E *)p.hidden;
     const int D = p.D;
     const float inv = 1.f / (float)D;
-    const bool tails = D % 8 != 0;
+    const bool odd = D % 8 != 0, tails = D < 8;
     float w[NV][8];
-    int n[NV];
+    Part pt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        n[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w<E>(p.weight, (i * L + l) * 8, n[i], tails, p.w_f32, w[i]);
+        pt[i] = Part(D, i * L + l);
+        load_w<E>(p.weight, pt[i].at, pt[i].n, tails, p.w_f32, w[i]);
         if (!GATED)
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[i][e] += p.offset;
@@ -76,18 +110,17 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E, 8, GATED && STREAM>(x + at + (i * L + l) * 8, n[i], tails);
+            xa[i] = load_n<E, 8, STREAM>(x + at + pt[i].at, pt[i].n, tails);
             if (GATED)
-                za[i] = load_n<E, 8, GATED && STREAM>(z + zat + (i * L + l) * 8, n[i], tails);
+                za[i] = load_n<E, 8, STREAM>(z + zat + pt[i].at, pt[i].n, tails);
             else if (res)
-                za[i] = load_n<E, 8, GATED && STREAM>(res + at + (i * L + l) * 8, n[i], tails);
+                za[i] = load_n<E, 8, STREAM>(res + at + pt[i].at, pt[i].n, tails);
         }
     };
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
     if (row < p.rows) load(row);
     for (int turn = 0; row < p.rows; row += groups, turn ^= 1) {
         float h[NV][8], g[NV][8];
-        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -95,8 +128,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                 h[i][e] = R::get(xa[i], e);
                 g[i][e] = GATED || res ? R::get(za[i], e) : 0.f;
                 if (!GATED) h[i][e] = fmaf(p.alpha, h[i][e], g[i][e]);
-                ss = fmaf(h[i][e], h[i][e], ss);
             }
+        const float ss = sum_own<NV>(h, h, pt, odd);
         if (row + groups < p.rows) load(row + groups);
         const float r = rsqrtf(group_sum<L>(ss, red, turn) * inv + p.eps);
         const int64_t at = row * D;
@@ -110,9 +143,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_kernel(NormParams p) {
                 R::set(o, e, v);
                 if (!GATED) R::set(ho, e, h[i][e]);
             }
-            store_n<E, 8, STREAM>(y + at + (i * L + l) * 8, o, n[i], tails);
+            store_n<E, 8, STREAM>(y + at + pt[i].at, o, pt[i].n, tails);
             if (!GATED)
-                if (hid) store_n<E, 8, STREAM>(hid + at + (i * L + l) * 8, ho, n[i], tails);
+                if (hid) store_n<E, 8, STREAM>(hid + at + pt[i].at, ho, pt[i].n, tails);
         }
     }
 }
@@ -131,13 +164,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
     E *__restrict__ dx = (E *)p.dx, *__restrict__ dz = (E *)(GATED ? p.dz : p.dresidual);
     const int D = p.D;
     const float inv = 1.f / (float)D;
-    const bool tails = D % 8 != 0;
+    const bool odd = D % 8 != 0, tails = D < 8;
     float w[NV][8], dw[NV][8];
-    int n[NV];
+    Part pt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        n[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w<E>(p.weight, (i * L + l) * 8, n[i], tails, p.w_f32, w[i]);
+        pt[i] = Part(D, i * L + l);
+        load_w<E>(p.weight, pt[i].at, pt[i].n, tails, p.w_f32, w[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (!GATED) w[i][e] += p.offset;
@@ -152,9 +185,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                                             (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E, 8, STREAM>(x + at + (i * L + l) * 8, n[i], tails);
-            da[i] = load_n<E, 8, STREAM>(dy + at + (i * L + l) * 8, n[i], tails);
-            if (GATED || z) za[i] = load_n<E, 8, STREAM>(z + zat + (i * L + l) * 8, n[i], tails);
+            xa[i] = load_n<E, 8, STREAM>(x + at + pt[i].at, pt[i].n, tails);
+            da[i] = load_n<E, 8, STREAM>(dy + at + pt[i].at, pt[i].n, tails);
+            if (GATED || z) za[i] = load_n<E, 8, STREAM>(z + zat + pt[i].at, pt[i].n, tails);
         }
     };
     // the longest rows have no registers left for the next row's loads (128 a thread)
@@ -172,8 +205,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                 h[i][e] = R::get(xa[i], e);
                 u[i][e] = R::get(da[i], e);
                 g[i][e] = GATED || z ? R::get(za[i], e) : 0.f;
-                ss = fmaf(h[i][e], h[i][e], ss);
                 const float t = GATED ? u[i][e] * w[i][e] * (g[i][e] * sigmoid_f(g[i][e])) : u[i][e] * w[i][e];
+                if (odd && e < pt[i].dup) continue;
+                ss = fmaf(h[i][e], h[i][e], ss);
                 sh = fmaf(t, h[i][e], sh);
             }
         if (AHEAD && row + groups < p.rows) load(row + groups);
@@ -199,8 +233,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
                     R::set(o, e, p.alpha * d);
                 }
             }
-            if (GATED || dx) store_n<E, 8, STREAM>(dx + at + (i * L + l) * 8, o, n[i], tails);
-            if (GATED || dz) store_n<E, 8, STREAM>(dz + at + (i * L + l) * 8, oz, n[i], tails);
+            if (GATED || dx) store_n<E, 8, STREAM>(dx + at + pt[i].at, o, pt[i].n, tails);
+            if (GATED || dz) store_n<E, 8, STREAM>(dz + at + pt[i].at, oz, pt[i].n, tails);
         }
     }
     // the workgroup's sums of dw: over its groups in order
@@ -210,13 +244,14 @@ __global__ void __launch_bounds__(threads_of(L)) norm_bwd_kernel(NormParams p) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < n[i]) part[(i * L + l) * 8 + e] = dw[i][e];
+                if (e >= pt[i].dup && e < pt[i].n) part[pt[i].at + e] = dw[i][e];
     } else {
         __shared__ float acc[GPB][L * NV * 8];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[threadIdx.x / L][(i * L + l) * 8 + e] = dw[i][e];
+            for (int e = 0; e < 8; ++e)
+                if (e >= pt[i].dup && e < pt[i].n) acc[threadIdx.x / L][pt[i].at + e] = dw[i][e];
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += NT) {
             float s = 0.f;
@@ -295,10 +330,9 @@ int norm_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L =
 int norm_bwd_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L == 1024 ? 4096 : 2048); }
 
 // Passes over more than the 256 MiB of the last cache are streamed past it: 16,384
-// rows of 5120 forward 120 against 125 us (stores only: streamed loads too, 123),
-// 4096 backward 127 against 135; 16,384 x 32 gated rows of 128 forward 75 against
-// 83, backward 126 against 133 (before the grids above).  Smaller outputs stay
-// there for their reader.
+// rows of 5120 forward 110 against 122 us (with plain loads 117), 16,383 of 4096
+// backward 114 against 127; 16,384 x 32 gated rows of 128 forward 67 against 77,
+// backward 111 against 129.  Smaller outputs stay there for their reader.
 bool streams(const NormParams &p, size_t elem, int tensors) { return (size_t)p.rows * p.D * elem * tensors > (256u << 20); }
 
 template <typename E, int L, int NV, bool GATED>

@@ -351,7 +351,7 @@ def test_conv_backward_matches_the_definition(name, dtype):
 @TYPES
 @pytest.mark.parametrize("lead,D", [((5, 4), 128), ((3, 1, 6), 64), ((7,), 1), ((2, 3), 100), ((9, 2), 129), ((3,), 512),
                                     ((2, 2), 777), ((2,), 1024), ((300, 32), 128), ((3, 5), 1021), ((700, 9), 5),
-                                    ((900, 10), 187), ((257, 9), 252)])
+                                    ((900, 10), 187), ((257, 9), 252), ((70, 3), 9), ((5, 2), 15)])
 def test_gated_norm_and_backward(lead, D, dtype):
     gdn = _gdn()
     d = Draw(D)
@@ -375,7 +375,7 @@ def test_gated_norm_and_backward(lead, D, dtype):
 @TYPES
 @pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (70, 64), (5, 520), (4, 1025), (3, 2048), (700, 2048), (2, 2500),
                                     (3, 4096), (2, 5121), (2, 8192), (3, 9001), (2, 16384), (2, 16383), (3, 1032),
-                                    (900, 1027), (600, 4097), (9000, 3), (400, 10240)])
+                                    (900, 1027), (600, 4097), (9000, 3), (400, 10240), (65, 9), (33, 15)])
 def test_add_norm_and_backward(rows, D, dtype):
     gdn = _gdn()
     d = Draw(rows + D)
