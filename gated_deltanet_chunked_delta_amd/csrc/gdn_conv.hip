@@ -40,11 +40,17 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int t, int T_t
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// One lane's C columns: of one piece of out (or of its gradient), fewer at the
-// piece's end.  A lane behind the last column reads what the last one reads and
-// stores nothing, so that a wave without piece ends (tails false) loads without a
-// condition.
-template <typename E, int C> struct Lane {
+// One lane's C columns of one piece of out (or of its gradient).  The last ones of
+// a piece whose size is no multiple of C begin inside the neighbour's, so that
+// accesses are whole vectors: both lanes compute and store the same values there.
+// Where a history is updated in place (INPLACE) that needs the neighbour in the
+// same wave, whose loads come before its stores.  Otherwise, and in a piece of
+// fewer than C columns, the lane has fewer columns (tails).  A lane behind the last
+// column reads what the last one reads and stores nothing, so that a wave without
+// tails loads without a condition (32,768 tokens of 4091 columns with the last ones
+// by fours, twos and one instead: 267 against 118 us, their gradients 569 against
+// 214).
+template <typename E, int C, bool INPLACE> struct Lane {
     int d, m, n;         // first column, columns to read, to store
     bool tails;
     E *ptr;              // column d in row 0 of the piece
@@ -62,9 +68,11 @@ template <typename E, int C> struct Lane {
         for (int i = 0; i < 3; ++i) {
             const int dim = p.piece_dim[i], nv = (dim + C - 1) / C, c = (v - v0) * C;
             if (v >= v0 && v < v0 + nv) {
-                d = c0 + c;
-                m = min(dim - c, C);
-                ptr = (E *)p.piece[i] + c;
+                const bool over = dim - c < C && dim >= C && !(INPLACE && (v & 63) == 0);
+                const int first = over ? dim - C : c;
+                d = c0 + first;
+                m = min(dim - first, C);
+                ptr = (E *)p.piece[i] + first;
                 stride = dim;
             }
             v0 += nv;
@@ -85,8 +93,8 @@ template <typename E, int C> struct Lane {
 };
 
 // The lane's weights and bias in fp32: w[j][e], b[e].
-template <typename E, int W, int C>
-__device__ __forceinline__ void load_weights(const ConvParams &p, const Lane<E, C> &ln, float (*w)[C], float *b) {
+template <int W, typename E, int C, bool I>
+__device__ __forceinline__ void load_weights(const ConvParams &p, const Lane<E, C, I> &ln, float (*w)[C], float *b) {
     // the lane's C W weights are consecutive
     float flat[W * C];
 #pragma unroll
@@ -102,8 +110,8 @@ __device__ __forceinline__ void load_weights(const ConvParams &p, const Lane<E, 
 }
 
 // A history [D, W-1] at `h`: row j (oldest first) of the lane's columns.
-template <typename E, int W, int C>
-__device__ __forceinline__ void load_history(const E *h, const Lane<E, C> &ln, float (*win)[C]) {
+template <int W, typename E, int C, bool I>
+__device__ __forceinline__ void load_history(const E *h, const Lane<E, C, I> &ln, float (*win)[C]) {
     float flat[(W - 1) * C];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -116,8 +124,8 @@ __device__ __forceinline__ void load_history(const E *h, const Lane<E, C> &ln, f
 #pragma unroll
         for (int e = 0; e < C; ++e) win[j][e] = flat[e * (W - 1) + j];
 }
-template <typename E, int W, int C>
-__device__ __forceinline__ void store_history(E *h, const Lane<E, C> &ln, const float (*win)[C]) {
+template <int W, typename E, int C, bool I>
+__device__ __forceinline__ void store_history(E *h, const Lane<E, C, I> &ln, const float (*win)[C]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         typename Raw<E, C>::T v;
@@ -141,15 +149,15 @@ template <typename E> __device__ __forceinline__ const E *start_of(const ConvPar
 
 // The W-1 rows before token t (as loaded; rows before the first token are not
 // meant), and the window they give for a sequence that begins at t0.
-template <typename E, int W, int C>
-__device__ __forceinline__ void load_before(const ConvParams &p, const E *x, int t, const Lane<E, C> &ln,
+template <int W, typename E, int C, bool I>
+__device__ __forceinline__ void load_before(const ConvParams &p, const E *x, int t, const Lane<E, C, I> &ln,
                                             typename Raw<E, C>::T *v) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) v[j] = ln.read(ln.in(x + (int64_t)max(t - (W - 1) + j, 0) * p.x_stride));
 }
-template <typename E, int W, int C>
+template <int W, typename E, int C, bool I>
 __device__ __forceinline__ void window_of(const ConvParams &p, const typename Raw<E, C>::T *v, int t, int t0,
-                                          const E *hist, const Lane<E, C> &ln, float (*win)[C]) {
+                                          const E *hist, const Lane<E, C, I> &ln, float (*win)[C]) {
     if (t - t0 >= W - 1) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -162,7 +170,7 @@ __device__ __forceinline__ void window_of(const ConvParams &p, const typename Ra
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
         for (int e = 0; e < C; ++e) old[j][e] = 0.f;
-    if (hist) load_history<E, W, C>(hist, ln, old);
+    if (hist) load_history<W>(hist, ln, old);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         // position t - t0 - (W-1) + j: a row, or history row t - t0 + j (constant indices keep it in registers)
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvParams p, int L, int nstr
     if (blk >= nmain) {   // final states
         const int64_t u = (int64_t)(blk - nmain) * 4 + wv;
         const int s = (int)(u / cblocks);
-        const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+        const Lane<E, C, true> ln(p, (int)(u % cblocks) * 64 + lane);
         if (s >= p.N || ln.n == 0) return;
         E *dst = (E *)start_of<E>(p, s, p.final_state);
         if (!dst) return;
@@ -253,13 +261,13 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvParams p, int L, int nstr
         seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
         float win[W - 1][C];
         V before[W - 1];
-        if (t1 > t0) load_before<E, W, C>(p, (const E *)p.x, t1, ln, before);
-        window_of<E, W, C>(p, before, t1, t0, start_of<E>(p, s, p.initial), ln, win);
-        store_history<E, W, C>(dst, ln, win);
+        if (t1 > t0) load_before<W>(p, (const E *)p.x, t1, ln, before);
+        window_of<W>(p, before, t1, t0, start_of<E>(p, s, p.initial), ln, win);
+        store_history<W>(dst, ln, win);
         return;
     }
     const int strip = (blk / cblocks) * 4 + wv;
-    const Lane<E, C> ln(p, (blk % cblocks) * 64 + lane);
+    const Lane<E, C, false> ln(p, (blk % cblocks) * 64 + lane);
     const int n = ln.n;
     if (strip >= nstrips) return;
     const int s0 = strip * L, s1 = min(s0 + L, tokens_of(p));
@@ -272,15 +280,15 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvParams p, int L, int nstr
         for (int i = 0; i < U; ++i)
             if (t + i < s1) xa[i] = ln.read(ln.in(x + (int64_t)(t + i) * p.x_stride));
     };
-    load_before<E, W, C>(p, x, s0, ln, before);
+    load_before<W>(p, x, s0, ln, before);
     load(s0);
     float w[W][C], b[C], win[W - 1][C];
-    load_weights<E, W, C>(p, ln, w, b);
+    load_weights<W>(p, ln, w, b);
     Walk at{p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T, 0, 0};
     if (n == 0) return;
     auto begin = [&](int r, bool first) {
         at.to(p, r, first);
-        window_of<E, W, C>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
+        window_of<W>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
     };
     auto step = [&](int r, const V &v) {
         float xv[C];
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
     // the first 64 slots of the row in the lanes, looked up while the rows load
     const int slots = idx[min(lane, sl.cols - 1)];
     const int a = sl.accepted ? min(max(sl.accepted[s], 1), sl.cols) : 1;
-    const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+    const Lane<E, C, true> ln(p, (int)(u % cblocks) * 64 + lane);
     const int n = ln.n;
     int t0, t1;
     seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
     };
     load(t0);
     float w[W][C], b[C], win[W - 1][C];
-    load_weights<E, W, C>(p, ln, w, b);
+    load_weights<W>(p, ln, w, b);
     const int slot = slot_of(__builtin_amdgcn_readfirstlane(a) - 1);
     if (slot < 0 || slot >= sl.pool_size) {   // padding row
         for (int t = t0; t < t1; ++t) ln.write(ln.row(t), R::zero());
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
     }
     E *pool = (E *)sl.data;
     const int64_t hist = (int64_t)p.D * (W - 1);
-    load_history<E, W, C>(pool + slot * hist, ln, win);
+    load_history<W>(pool + slot * hist, ln, win);
     for (int t = t0; t < t1; t += U) {
         if (t > t0) load(t);
 #pragma unroll
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
             const int c = min(t + i - t0, sl.cols - 1);
             if (c < sl.cols - 1 || t + i == t1 - 1) {
                 const int to = slot_of(c);
-                if (to >= 0 && to < sl.pool_size) store_history<E, W, C>(pool + to * hist, ln, win);
+                if (to >= 0 && to < sl.pool_size) store_history<W>(pool + to * hist, ln, win);
             }
         }
     }
@@ -407,19 +415,19 @@ conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
     if (blk >= nmain) {   // gradients of the start histories
         const int64_t u = (int64_t)(blk - nmain) * 4 + wv;
         const int s = (int)(u / cblocks);
-        const Lane<E, C> ln(p, (int)(u % cblocks) * 64 + lane);
+        const Lane<E, C, false> ln(p, (int)(u % cblocks) * 64 + lane);
         const int n = ln.n;
         if (s >= p.N || n == 0) return;
         int t0, t1;
         seq_range(p.cu_seqlens, s, p.T, p.T_tot, t0, t1);
         const E *x = (const E *)p.x;
         float w[W][C], b[C], win[W - 1][C], g[W - 1][C];
-        load_weights<E, W, C>(p, ln, w, b);
+        load_weights<W>(p, ln, w, b);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
             for (int e = 0; e < C; ++e) g[i][e] = win[i][e] = 0.f;
-        if (const E *h = start_of<E>(p, s, p.initial)) load_history<E, W, C>(h, ln, win);
+        if (const E *h = start_of<E>(p, s, p.initial)) load_history<W>(h, ln, win);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
             if (t0 + i < t1) {
@@ -437,12 +445,12 @@ conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
                 }
                 shift_in<W, C>(win, xv);
             }
-        store_history<E, W, C>((E *)p.dinitial + (int64_t)s * p.D * (W - 1), ln, g);
+        store_history<W>((E *)p.dinitial + (int64_t)s * p.D * (W - 1), ln, g);
         return;
     }
     __shared__ float red[4][W + 1][64 * C];
     const int group = blk / cblocks, strip = group * 4 + wv;
-    const Lane<E, C> ln(p, (blk % cblocks) * 64 + lane);
+    const Lane<E, C, false> ln(p, (blk % cblocks) * 64 + lane);
     const int n = ln.n;
     float dw[W + 1][C];
 #pragma unroll
@@ -463,10 +471,10 @@ conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
                     da[i] = ln.template read<STREAM>(ln.row(t + i));
                 }
         };
-        load_before<E, W, C>(p, x, s0, ln, before);
+        load_before<W>(p, x, s0, ln, before);
         load(s0);
         float w[W][C], b[C], win[W - 1][C], acc[W - 1][C];
-        load_weights<E, W, C>(p, ln, w, b);
+        load_weights<W>(p, ln, w, b);
         Walk at{p.cu_seqlens ? find_seq(p.cu_seqlens, p.N, s0, p.T_tot) : s0 / p.T, 0, 0};
         int ta = s0;                                   // the sequence's first token in the strip
         auto put = [&](int row, const float *v) {
@@ -478,7 +486,7 @@ conv_bwd_kernel(ConvParams p, int L, int nstrips, int cblocks, int nmain) {
         auto begin = [&](int r, bool first) {
             at.to(p, r, first);
             ta = r;
-            window_of<E, W, C>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
+            window_of<W>(p, before, r, at.t0, start_of<E>(p, at.seq, p.initial), ln, win);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -592,6 +600,15 @@ int bwd_groups(int64_t T_tot, int64_t D, int W) {
 bool streams(const ConvParams &p, size_t elem, int tensors) {
     return (size_t)p.T_tot * p.D * elem * tensors > (256u << 20);
 }
+// The backward pass streams its loads too, which pays only if no two waves share a
+// line of a row: rows of whole 64 bytes (16,384 tokens of 8192 columns above; 32,768
+// of 4091 236 us streamed, 214 not).
+bool whole_lines(const ConvParams &p, size_t elem) {
+    const size_t m = 64 / elem;
+    bool whole = p.D % m == 0 && p.x_stride % m == 0;
+    for (int i = 0; i < 3; ++i) whole = whole && p.piece_dim[i] % m == 0;
+    return whole;
+}
 
 template <typename E, int W>
 void launch_fwd_cfg(const ConvParams &p, hipStream_t st, Profiler *prof) {
@@ -621,7 +638,7 @@ void launch_bwd_cfg(const ConvParams &p, int L, hipStream_t st) {
     const int cb = lane_blocks(p, kBwdCols);
     const int nstrips = (p.T_tot + L - 1) / L, nmain = (nstrips + 3) / 4 * cb;
     const int nfin = p.dinitial ? (int)(((int64_t)p.N * cb + 3) / 4) : 0;
-    if (streams(p, sizeof(E), 3))
+    if (streams(p, sizeof(E), 3) && whole_lines(p, sizeof(E)))
         conv_bwd_kernel<E, W, true><<<nmain + nfin, 256, 0, st>>>(p, L, nstrips, cb, nmain);
     else
         conv_bwd_kernel<E, W, false><<<nmain + nfin, 256, 0, st>>>(p, L, nstrips, cb, nmain);

@@ -219,6 +219,10 @@ CONV = {   # lengths (a tuple: equal), D, W, bias, initial, split, extra columns
     "no_silu": ([33, 31], 520, 2, True, False, (8, 512), 0, False),
     "many": ([i % 4 for i in range(300)], 40, 4, False, True, None, 0, True),
     "one_token": ((1,) * 5, 136, 4, True, True, None, 0, True),
+    # pieces that end one to three columns into a wave, pieces of fewer columns than a lane's
+    "wave_border": ([1, 0, 2, 40, 1, 1], 779, 4, True, True, (515, 5, 259), 0, True),
+    "few_columns": ((2, 2, 2), 13, 3, False, True, (7, 3, 3), 1, True),
+    "last_parts": ([3, 1, 70, 2], 1043, 4, False, True, (521, 9, 513), 5, True),
 }
 
 
@@ -288,6 +292,8 @@ UPDATE = {   # lengths, D, W, columns, bias, split, extra
     "drafts": ((4,) * 5, 1000, 4, 4, True, None, 24),
     "ragged": ([2, 0, 5, 1, 3], 515, 3, 3, True, (100, 200, 215), 1),
     "long": ([19, 40], 16, 2, 1, False, None, 0),
+    "wave_border": ((1,) * 40, 518, 4, 1, True, (259, 3, 256), 0),
+    "last_parts": ((3,) * 21, 1043, 4, 2, False, (517, 9, 517), 3),
 }
 
 
