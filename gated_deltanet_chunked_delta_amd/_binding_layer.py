@@ -501,10 +501,10 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, cu_seqlens=N
     lib = _lib or _load()
     need = lib.gdn_conv_bwd_workspace_bytes(_addr(shape))
     ws = _workspace(workspace, need, dev, x)
-    dx = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
-    dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-    dbias = None if bias is None else torch.empty(D, dtype=torch.float32, device=x.device)
-    dinitial = torch.empty(slot, dtype=x.dtype, device=x.device) if output_dinitial else None
+    dx = x.new_empty((B, T, D))
+    dweight = torch.empty_like(weight, dtype=torch.float32)
+    dbias = None if bias is None else torch.empty_like(bias, dtype=torch.float32)
+    dinitial = x.new_empty(slot) if output_dinitial else None
     _run(dev, lib.gdn_conv_bwd, rows.data_ptr(), weight.data_ptr(), _p(bias), activation is not None,
          _p(initial_state), _p(cu), _addr(pieces), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dinitial), _addr(shape),
          ws.data_ptr(), need)
@@ -586,7 +586,7 @@ def fused_gated_rms_norm_bwd(x, z, weight, dy, eps=1e-6, workspace=None):
     need = lib.gdn_norm_bwd_workspace_bytes(_addr(shape))
     ws = _workspace(workspace, need, dev, x)
     dx, dz = torch.empty_like(x), torch.empty_like(x)
-    dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+    dweight = torch.empty_like(weight, dtype=torch.float32)
     _run(dev, lib.gdn_gated_norm_bwd, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, dy.data_ptr(), dx.data_ptr(),
          dz.data_ptr(), dweight.data_ptr(), _addr(shape), ws.data_ptr(), need)
     return dx, dz, dweight
@@ -628,7 +628,7 @@ def fused_add_rms_norm_bwd(dy, dhidden, hidden, weight, eps=1e-6, residual_scale
     ws = _workspace(workspace, need, dev, hidden)
     dx = torch.empty_like(hidden) if output_dx else None
     dresidual = torch.empty_like(hidden)
-    dweight = torch.empty(weight.shape, dtype=torch.float32, device=hidden.device)
+    dweight = torch.empty_like(weight, dtype=torch.float32)
     _run(dev, lib.gdn_add_norm_bwd, dy.data_ptr(), _p(dhidden), hidden.data_ptr(), weight.data_ptr(), residual_scale,
          weight_offset, eps, _p(dx), dresidual.data_ptr(), dweight.data_ptr(), _addr(shape), ws.data_ptr(), need)
     return dx, dresidual, dweight
