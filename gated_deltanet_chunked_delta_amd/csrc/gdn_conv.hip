@@ -572,13 +572,14 @@ int lane_blocks(const ConvParams &p, int C) {
     for (int i = 0; i < 3; ++i) v += ((int64_t)p.piece_dim[i] + C - 1) / C;
     return (int)((v + 63) / 64);
 }
-constexpr int kStripWaves = 4096;
+constexpr int kStripWaves = 2048;
 // Tokens of a strip: whole load batches; 12 or 16 forward and 48 or 64 backward
 // (W = 4: 16,384 tokens of 3392 columns and 5036 a sequence forward 159 us, with
 // 24 163, with 6 172; the gradients of 16,384 tokens of 8192 columns 173, with 96
 // 180, with 24 182: longer ones leave a CU's rows far apart, shorter ones read
 // more rows twice and leave more partial sums), fewer where that leaves less than
-// 4096 waves.
+// 2048 waves (the gradients of 1024 tokens of 4096 columns 18 us, with 4096 waves 24;
+// of 8170 of 1152 fp32 19.5 against 24; of 32,768 of 816 53 against 58).
 int strip_len(int64_t T_tot, int64_t D, int C, int lo, int hi) {
     int L = hi;
     while (L > lo && ((T_tot + L - 1) / L) * col_blocks(D, C) < kStripWaves) L >>= 1;
