@@ -16,7 +16,9 @@
 // rows are then in the CU's cache).  Strips ignore the sequences' borders: a
 // strip finds its first sequence by a 64-way search over cu_seqlens and
 // restarts its window where a sequence begins, so packed batches need no
-// schedule.  Arithmetic is fp32, each output rounded once.
+// schedule.  Arithmetic is fp32, each output rounded once.  64 packed prompts (62,386
+// tokens) of 8192 bf16 columns take 435 us, 5.6 TB/s; the gradients of 16,384 tokens
+// 175 us, 4.7 TB/s; 256 decode rows 11.1 us, 3 TB/s (slot, then history).
 #include "gdn_layer_device.h"
 
 namespace gdn {
@@ -400,8 +402,9 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvParams p, int cblo
 // dweight and dbias through LDS into one row of the workspace.  A lane has four
 // columns: windows, weights and sums are 4 W + 1 floats a column, and with eight
 // columns one or two waves are left a SIMD to hide the loads behind (16,384
-// tokens of 8192 columns 246 us, with four 191; three waves a SIMD instead of two
-// another 8 % where the tokens do not fill the card evenly).
+// tokens of 8192 columns 246 us, with four 191 and with the strips and streaming
+// below 175; three waves a SIMD instead of two another 8 % where the tokens do not
+// fill the card evenly).
 constexpr int kBwdCols = 4;
 
 template <typename E, int W, bool STREAM>
