@@ -16,7 +16,7 @@
 // rows are then in the CU's cache).  Strips ignore the sequences' borders: a
 // strip finds its first sequence by a 64-way search over cu_seqlens and
 // restarts its window where a sequence begins, so packed batches need no
-// schedule.  Arithmetic is fp32, each output rounded once.  64 packed prompts (62,386
+// schedule.  Arithmetic is fp32, each output rounded once.  64 packed prompts (73,844
 // tokens) of 8192 bf16 columns take 435 us, 5.6 TB/s; the gradients of 16,384 tokens
 // 175 us, 4.7 TB/s; 256 decode rows 11.1 us, 3 TB/s (slot, then history).
 #include "gdn_layer_device.h"
@@ -577,12 +577,12 @@ int lane_blocks(const ConvParams &p, int C) {
 }
 constexpr int kStripWaves = 2048;
 // Tokens of a strip: whole load batches; 12 or 16 forward and 48 or 64 backward
-// (W = 4: 16,384 tokens of 3392 columns and 5036 a sequence forward 159 us, with
+// (W = 4: 46,303 packed tokens of 4544 columns forward 159 us, with
 // 24 163, with 6 172; the gradients of 16,384 tokens of 8192 columns 173, with 96
 // 180, with 24 182: longer ones leave a CU's rows far apart, shorter ones read
 // more rows twice and leave more partial sums), fewer where that leaves less than
 // 2048 waves (the gradients of 1024 tokens of 4096 columns 18 us, with 4096 waves 24;
-// of 8170 of 1152 fp32 19.5 against 24; of 32,768 of 816 53 against 58).
+// of 2,956 of 1152 fp32 19.5 against 24; of 32,768 of 816 53 against 58).
 int strip_len(int64_t T_tot, int64_t D, int C, int lo, int hi) {
     int L = hi;
     while (L > lo && ((T_tot + L - 1) / L) * col_blocks(D, C) < kStripWaves) L >>= 1;
@@ -598,7 +598,7 @@ int bwd_groups(int64_t T_tot, int64_t D, int W) {
 }
 
 // Passes over more than the 256 MiB of the last cache are streamed past it (the
-// forward pass its outputs only: the strips share rows of x): 62,386 packed
+// forward pass its outputs only: the strips share rows of x): 73,844 packed
 // tokens of 8192 columns 437 against 459 us, the gradients of 16,384 tokens 175
 // against 182.
 bool streams(const ConvParams &p, size_t elem, int tensors) {
