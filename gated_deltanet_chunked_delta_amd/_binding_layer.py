@@ -565,7 +565,9 @@ def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
 
     x, z [..., D] of one shape and dtype (bf16 or fp32, D up to 1024), as the
     delta rule's output [B,T,HV,V] and its gate, which may be a part of a wider
-    projection's rows; weight [D] in x's dtype or float32.  Returns x's shape."""
+    projection's rows; weight [D] in x's dtype or float32.  Returns x's shape.  A
+    row whose squares sum to infinity in fp32 gives zeros, and NaN where it is
+    infinite; its gradients are undefined."""
     dev, shape, weight = _norm_args(x, weight)
     z = _gate_rows(x, z, shape)
     x = x.contiguous()
@@ -598,7 +600,8 @@ def fused_add_rms_norm(x, residual, weight, eps=1e-6, residual_scale=1.0, weight
     x, residual [..., D] of one shape and dtype (bf16 or fp32, D up to 16384);
     residual may be None (zeros).  Returns ``(y, hidden)``, y = hidden / rms *
     (weight + weight_offset), taken from the unrounded hidden.  ``hidden`` may be
-    the residual itself, which is then updated in place."""
+    the residual itself, which is then updated in place.  Rows whose squares sum to
+    infinity as in fused_gated_rms_norm."""
     dev, shape, weight = _norm_args(x, weight)
     if residual is not None:
         residual = _same(x, residual, "residual")

@@ -62,14 +62,15 @@ struct Part {
         n = min(max(D - at, 0), 8);
     }
 };
-// Sum of a b over the lane's own elements.
+// Sum of a b over the lane's own elements (chosen, not multiplied by zero: an infinity
+// among the others is the neighbour's).
 template <int NV> __device__ __forceinline__ float sum_own(const float (*a)[8], const float (*b)[8], const Part *pt, bool odd) {
     float s = 0.f;
     if (odd) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(e >= pt[i].dup ? a[i][e] : 0.f, b[i][e], s);
+            for (int e = 0; e < 8; ++e) s = e >= pt[i].dup ? fmaf(a[i][e], b[i][e], s) : s;
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)

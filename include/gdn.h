@@ -584,10 +584,11 @@ typedef struct gdn_norm_shape {
  *
  *   x, out        [rows, D] dtype;  z  see gdn_norm_shape;  weight [D] weight_dtype
  *
- * Tensors are aligned to their element; out must not overlap an input.  The
- * squares of a row have to sum to a finite fp32.  Returns GDN_OK, GDN_ERR_NULL,
- * GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or
- * GDN_ERR_LAUNCH. */
+ * Tensors are aligned to their element; out must not overlap an input.  Where
+ * the squares of a row sum to infinity in fp32, r is 0: its finite elements give
+ * zeros and an infinite one NaN (the gradients of such a row are undefined).
+ * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
 int gdn_gated_norm(const void *x, const void *z, const void *weight, float eps, void *out,
                    const gdn_norm_shape *shape, void *stream);
 
