@@ -247,6 +247,32 @@ def _given(t, shape, x, dev, name):
     return t
 
 
+def _span(t):
+    """First byte of t and one past its last."""
+    at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.nbytes
+    return at, at + t.element_size() * (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())))
+
+
+def _apart(name, written, *read, same=()):
+    """Refuses tensors to be written that overlap each other, one of read, or one
+    of same without being the same elements: another workgroup may not have read
+    them yet."""
+    spans = [_span(t) for t in read if t is not None]
+    for t in written:
+        a0, a1 = span = _span(t)
+        for b0, b1 in spans:
+            if b0 < a1 and a0 < b1:
+                raise ValueError(f"{name} must not overlap an input or another output")
+        spans.append(span)
+        for u in same:
+            if u is not None and (u.data_ptr() != a0 or not u.is_contiguous()):
+                b0, b1 = _span(u)
+                if b0 < a1 and a0 < b1:
+                    raise ValueError(f"{name} must not overlap a part of an input")
+
+
 def _workspace(workspace, need, dev, x):
     """The caller's workspace where it is large enough, else a new one."""
     if workspace is None or workspace.numel() * workspace.element_size() < need:
@@ -273,7 +299,8 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
     (column 0 without ``num_accepted``, int32 [N], taken into [1, cols]); column
     c < cols - 1 then holds the state after its token c + 1, the last column the
     state after its last token.  A start slot outside [0, P) marks a padding
-    row: zeros in the output, nothing stored.  Returns o with v's shape.
+    row: zeros in the output, nothing stored.  Returns o with v's shape; ``out``,
+    used as given, must not overlap the inputs or the pool.
     """
     dims, vdims, dt = q.shape, v.shape, q.dtype
     if len(dims) != 4 or k.shape != dims:
@@ -314,7 +341,10 @@ def fused_recurrent_gated_delta_rule_steps(q, k, v, g, beta, state_pool, state_i
         raise ValueError("state_pool must be float32 or bfloat16")
     pool, kept = _step_pool(dev, state_pool, state_indices, num_accepted, N, (HV, K, V), "state_pool")
     q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-    out = torch.empty_like(v) if out is None else _given(out, vdims, v, dev, "out")
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _apart("out", [_given(out, vdims, v, dev, "out")], q, k, g, beta, state_pool, same=(v,))
     if cu_seqlens is not None:
         cu_seqlens = cu_seqlens.contiguous()
     shape = gdn_shape(B, T, H, HV, K, V, N, code)
@@ -406,7 +436,7 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
     [B,T,D], or with ``split_sizes`` (up to three, summing to D) a tuple of
     contiguous [B,T,size] tensors, ready as q, k and v; final_state [N,D,W-1] or
     None.  ``out`` and ``final_state`` (which may be initial_state) are used as
-    given.
+    given; they must not overlap the inputs, the pool or each other.
 
     With ``conv_state_pool`` [P,D,W-1] and ``conv_state_indices`` [N] int32,
     sequence n starts from slot conv_state_indices[n] (from zeros if
@@ -417,6 +447,8 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
     D, W1 = x.shape[2], shape.W - 1
     outs, pieces = _pieces(x, (D,) if split_sizes is None else split_sizes, _listed(out), dev, "out")
     y = outs[0] if split_sizes is None else tuple(outs)
+    if out is not None:
+        _apart("out", outs, rows, weight, bias, initial_state, conv_state_pool)
     lib = _lib or _load()
     head = (rows.data_ptr(), weight.data_ptr(), _p(bias), activation is not None)
     if conv_state_pool is not None:
@@ -437,7 +469,8 @@ def causal_conv1d(x, weight, bias=None, initial_state=None, output_final_state=T
     if not output_final_state:
         final_state = None
     elif final_state is not None:
-        _given(final_state, (N, D, W1), x, dev, "final_state")
+        _apart("final_state", [_given(final_state, (N, D, W1), x, dev, "final_state")], rows, weight, bias, *outs,
+               same=(initial_state,))
     elif initial_state is not None:
         final_state = torch.empty_like(initial_state)
     else:
@@ -455,8 +488,8 @@ def causal_conv1d_update(x, weight, conv_state_pool, conv_state_indices, bias=No
     [P,D,W-1] in x's dtype, updated in place; conv_state_indices int32 [N] or
     [N,cols] and ``num_accepted`` as for fused_recurrent_gated_delta_rule_steps:
     the start slot, the slots that keep the history after each token, and padding
-    rows (zeros, nothing stored).  Returns y with x's shape, or a tuple of
-    [..., size] tensors.
+    rows (zeros, nothing stored).  ``out`` as for causal_conv1d.  Returns y with
+    x's shape, or a tuple of [..., size] tensors.
     """
     flat = x.dim() == 2
     out = _listed(out)
@@ -472,6 +505,8 @@ def causal_conv1d_update(x, weight, conv_state_pool, conv_state_indices, bias=No
     pool, kept = _step_pool(dev, conv_state_pool, conv_state_indices, num_accepted, N, (D, shape.W - 1),
                             "conv_state_pool")
     outs, pieces = _pieces(x, (D,) if split_sizes is None else split_sizes, out, dev, "out")
+    if out is not None:
+        _apart("out", outs, rows, weight, bias, conv_state_pool)
     _run(dev, (_lib or _load()).gdn_conv_update, rows.data_ptr(), weight.data_ptr(), _p(bias),
          activation is not None, _addr(pool), _p(cu), _addr(pieces), _addr(shape))
     if flat:
@@ -571,7 +606,10 @@ def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
     dev, shape, weight = _norm_args(x, weight)
     z = _gate_rows(x, z, shape)
     x = x.contiguous()
-    out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _apart("out", [_given(out, x.shape, x, dev, "out")], weight, same=(x, z))
     _run(dev, (_lib or _load()).gdn_gated_norm, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, out.data_ptr(),
          _addr(shape))
     return out
@@ -606,8 +644,11 @@ def fused_add_rms_norm(x, residual, weight, eps=1e-6, residual_scale=1.0, weight
     if residual is not None:
         residual = _same(x, residual, "residual")
     x = x.contiguous()
+    given = out is not None or (hidden is not None and hidden is not residual)
     out = torch.empty_like(x) if out is None else _given(out, x.shape, x, dev, "out")
     hidden = torch.empty_like(x) if hidden is None else _given(hidden, x.shape, x, dev, "hidden")
+    if given:
+        _apart("out and hidden", [out, hidden], weight, same=(x, residual))
     _run(dev, (_lib or _load()).gdn_add_norm, x.data_ptr(), _p(residual), weight.data_ptr(), residual_scale,
          weight_offset, eps, out.data_ptr(), hidden.data_ptr(), _addr(shape))
     return out, hidden

@@ -512,6 +512,9 @@ typedef struct gdn_conv_pieces {
  *                 (an empty sequence's is its initial state); may alias
  *                 initial_state exactly, must not overlap anything else
  *
+ * The parts of out must not overlap each other, x, weight, bias, the states or (in
+ * the calls below) the pool: a strip reads the W-1 rows before its own, which
+ * another one may have written.
  * Tensors are aligned to their element.  Arithmetic is fp32, rounded once.  No
  * workspace.  Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a
  * sequence, more than 2^31 - 65 of them, or too many for one launch: 2^24 - 1
@@ -533,7 +536,7 @@ int gdn_conv_fwd_pool(const void *x, const void *weight, const void *bias, int s
 /* The convolution of a few tokens per sequence with the histories in a pool
  * (causal_conv1d_update of the same pages), next to gdn_recurrent_update and
  * gdn_recurrent_steps: see gdn_step_pool, whose dtype is the shape's.  A
- * sequence's tokens are taken in order by one wave. */
+ * sequence's tokens are taken in order by one wave.  out as for gdn_conv_fwd. */
 int gdn_conv_update(const void *x, const void *weight, const void *bias, int silu,
                     const gdn_step_pool *pool, const int32_t *cu_seqlens,
                     const gdn_conv_pieces *out, const gdn_conv_shape *shape, void *stream);
