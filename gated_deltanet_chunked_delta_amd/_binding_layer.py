@@ -274,11 +274,13 @@ def _apart(name, written, *read, same=()):
 
 
 def _workspace(workspace, need, dev, x):
-    """The caller's workspace where it is large enough, else a new one."""
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
+    """The caller's workspace after its checks, or a new one."""
+    if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous buffer on cuda:{dev}")
+    if workspace.nbytes < need:
+        raise ValueError(f"workspace must have {need} bytes")
     return workspace
 
 
@@ -522,7 +524,7 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, cu_seqlens=N
     Returns ``(dx, dweight, dbias, dinitial)``: dx [B,T,D] in x's dtype, dweight
     [D,W] and dbias [D] float32 (None without bias), dinitial [N,D,W-1] in x's
     dtype (None unless ``output_dinitial``).  A preallocated uint8 ``workspace``
-    of gdn_conv_bwd_workspace_bytes bytes may be given.
+    of gdn_conv_bwd_workspace_bytes bytes or more, 16-byte aligned, may be given.
     """
     dev, rows, weight, bias, cu, shape, N = _conv_args(x, weight, bias, cu_seqlens, activation)
     B, T, D = x.shape
@@ -618,7 +620,8 @@ def fused_gated_rms_norm(x, z, weight, eps=1e-6, out=None):
 def fused_gated_rms_norm_bwd(x, z, weight, dy, eps=1e-6, workspace=None):
     """Backward pass of ``fused_gated_rms_norm``: ``(dx, dz, dweight)``, dx and
     dz in x's dtype and shape, dweight float32 [D].  A preallocated uint8
-    ``workspace`` of gdn_norm_bwd_workspace_bytes bytes may be given."""
+    ``workspace`` of gdn_norm_bwd_workspace_bytes bytes or more, 16-byte aligned,
+    may be given."""
     dev, shape, weight = _norm_args(x, weight)
     z = _gate_rows(x, z, shape)
     x, dy = x.contiguous(), _same(x, dy, "dy")
