@@ -83,8 +83,11 @@ def _r(s):
     return None if s is None else ctypes.addressof(s)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
 _addr = ctypes.addressof
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)   # looked up here: a torch without GPU support has none
 
 
 def _stream_of(t, stream):
