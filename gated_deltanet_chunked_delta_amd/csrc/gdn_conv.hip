@@ -18,7 +18,7 @@
 // restarts its window where a sequence begins, so packed batches need no
 // schedule.  Arithmetic is fp32, each output rounded once.  64 packed prompts (73,844
 // tokens) of 8192 bf16 columns take 435 us, 5.6 TB/s; the gradients of 16,384 tokens
-// 175 us, 4.7 TB/s; 256 decode rows 11.1 us, 3 TB/s (slot, then history).
+// 175 us, 4.6 TB/s; 256 decode rows 11 us, 3 TB/s (slot, then history).
 #include "gdn_layer_device.h"
 
 namespace gdn {
