@@ -84,10 +84,7 @@ def _r(s):
 
 
 _addr = ctypes.addressof
-
-
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)   # looked up here: a torch without GPU support has none
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # none in a torch without GPU support
 
 
 def _stream_of(t, stream):
