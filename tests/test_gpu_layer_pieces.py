@@ -60,3 +60,37 @@ def test_decode_layer_piece_by_piece(dtype):
 
     zs = z.unflatten(-1, (HV, V))
     _near("out", gdn.fused_gated_rms_norm(o, zs, t["w_out"].to(dtype)), *layer.gated_norm(o, zs, t["w_out"].to(dtype)), 64)
+
+
+def test_prompts_on_the_pool_in_a_graph():
+    """A packed prefill of the convolution on its pool, captured: the final states' launch overwrites the histories
+    that the strips read, on every replay; sequences over many strips, padding rows and an empty sequence."""
+    gdn = _gdn()
+    d, lens, D = Draw(17), [1, 700, 0, 3, 1290, 2, 64], 1040
+    N, T = len(lens), sum(lens)
+    x, w = d.randn(1, T, D, dtype=BF).to(DEV), d.randn(D, 4, std=0.5, dtype=BF).to(DEV)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(DEV)
+    idx = torch.tensor([3, 0, 7, -1, 5, 9, 2], dtype=torch.int32, device=DEV)     # 9 lies outside
+    pool0 = d.randn(8, D, 3, dtype=BF).to(DEV)
+    pool = pool0.clone()
+    step = lambda: gdn.causal_conv1d(x, w, cu_seqlens=cu, conv_state_pool=pool, conv_state_indices=idx)[0]
+    runs = []
+    for _ in range(2):     # from pool0, then from what the first run left
+        y = step()
+        runs.append((y.clone(), pool.clone()))
+    start = torch.stack([pool0[i] if 0 <= i < 8 else torch.zeros_like(pool0[0]) for i in idx.tolist()])
+    want, final = gdn.causal_conv1d(x, w, initial_state=start, cu_seqlens=cu)
+    assert torch.equal(runs[0][0], want) and torch.equal(runs[0][1][idx[idx.ge(0) & idx.lt(8)].long()],
+                                                         final[idx.ge(0) & idx.lt(8)])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        pool.copy_(pool0)
+        for want in runs:
+            out.fill_(7)
+            torch.randn(1 << 20, device=DEV).mul_(2.0).sum().item()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(pool, want[1]), f"replay {i}"
