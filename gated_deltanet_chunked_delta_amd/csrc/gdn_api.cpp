@@ -472,6 +472,110 @@ int check_norm_ws(const gdn_norm_shape &s, const float *dweight, const void *wor
     return GDN_OK;
 }
 
+// Sizes of a gated linear recurrence.
+int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with_beta) {
+    if (!shape) return GDN_ERR_NULL;
+    const gdn_scan_shape &s = *shape;
+    if (s.B < 0 || s.T < 0 || s.N < 0 || s.D <= 0 || s.D > (1 << 26)) return GDN_ERR_SHAPE;
+    if (gdn::elem_bytes(s.dtype) == 0 || gdn::elem_bytes(s.gate_dtype) == 0) return GDN_ERR_DTYPE;
+    if (s.gate_dtype != s.dtype && s.gate_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+    if (cu_seqlens ? s.B != 1 : s.N != s.B) return GDN_ERR_SHAPE;
+    const int64_t tokens = (int64_t)s.B * s.T, most = (int64_t)1 << 31;
+    if (tokens > INT_MAX - 64 || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
+    if (tokens > 0 && (s.x_stride < s.D || s.g_stride < s.D || (with_beta && s.beta_stride < s.D))) return GDN_ERR_SHAPE;
+    if (s.x_stride > most || s.g_stride > most || (with_beta && s.beta_stride > most)) return GDN_ERR_SHAPE;
+    if (gdn::scan_grid(tokens, s.D, s.N) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (((uintptr_t)cu_seqlens & 3u) != 0) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+gdn::ScanParams scan_params(const gdn_scan_shape &s, const void *x, const void *g, const void *beta,
+                            const int32_t *cu_seqlens) {
+    gdn::ScanParams p{};
+    p.x = x;
+    p.g = g;
+    p.beta = beta;
+    p.x_stride = s.x_stride;
+    p.g_stride = s.g_stride;
+    p.beta_stride = s.beta_stride;
+    p.cu_seqlens = cu_seqlens;
+    p.T = s.T;
+    p.T_tot = s.B * s.T;
+    p.D = s.D;
+    p.N = s.N;
+    return p;
+}
+int scan_gate_f32(const gdn_scan_shape &s) { return s.gate_dtype == GDN_F32; }
+int check_scan_ws(const gdn_scan_shape &s, bool backward, const void *workspace, size_t workspace_bytes) {
+    const size_t need =
+        gdn::scan_workspace_bytes((int64_t)s.B * s.T, s.D, s.dtype, scan_gate_f32(s), backward);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GDN_ERR_WORKSPACE;
+    return GDN_OK;
+}
+
+int scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state, const gdn_state_pool *pool,
+             const int32_t *cu_seqlens, void *out, float *final_state, const gdn_scan_shape *shape, void *workspace,
+             size_t workspace_bytes, void *stream) {
+    int st = check_scan(shape, cu_seqlens, beta != nullptr);
+    if (st != GDN_OK) return st;
+    const gdn_scan_shape &s = *shape;
+    if ((int64_t)s.B * s.T > 0 && (!x || !g || !out)) return GDN_ERR_NULL;
+    if (misaligned(s.dtype, x, out) || misaligned(s.gate_dtype, g, beta) ||
+        misaligned(GDN_F32, initial_state, final_state))
+        return GDN_ERR_ALIGN;
+    gdn::ScanParams p = scan_params(s, x, g, beta, cu_seqlens);
+    p.y = out;
+    p.initial = initial_state;
+    p.final_state = final_state;
+    if (pool && s.N > 0) {
+        if (!pool->data || !pool->indices) return GDN_ERR_NULL;
+        if (gdn::elem_bytes(pool->dtype) == 0) return GDN_ERR_DTYPE;
+        if (pool->pool_size < 1) return GDN_ERR_SHAPE;
+        if (misaligned(pool->dtype, pool->data) || misaligned(GDN_F32, pool->indices)) return GDN_ERR_ALIGN;
+        p.initial = pool->read_initial ? pool->data : nullptr;
+        p.final_state = pool->data;
+        p.indices = pool->indices;
+        p.pool_size = pool->pool_size;
+        p.state_bf16 = pool->dtype == GDN_BF16;
+    }
+    st = check_scan_ws(s, false, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    p.ws = workspace;
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_scan(p, s.dtype, scan_gate_f32(s), (hipStream_t)stream, prof);
+    });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// Tensors of codes and scales; nothing to check where there are no rows.
+int check_held(const gdn_held *h, bool any) {
+    if (!h || (any && (!h->codes || !h->scales))) return GDN_ERR_NULL;
+    return ((uintptr_t)h->scales & 1u) != 0 ? GDN_ERR_ALIGN : GDN_OK;
+}
+gdn::Held held_of(const gdn_held &h) { return gdn::Held{h.codes, h.scales}; }
+
+int hold(void *values, const int32_t *value_index, const gdn_held *held, const int32_t *held_index,
+         const gdn_held_shape *shape, bool back, void *stream) {
+    if (!shape) return GDN_ERR_NULL;
+    const gdn_held_shape &s = *shape;
+    if (s.n < 0 || s.D <= 0 || s.D > INT_MAX || s.value_rows < 0 || s.held_rows < 0) return GDN_ERR_SHAPE;
+    if (gdn::elem_bytes(s.dtype) == 0) return GDN_ERR_DTYPE;
+    if (s.bits != 8 && s.bits != 4) return GDN_ERR_UNSUPPORTED;
+    if (s.n == 0) return GDN_OK;
+    if (s.stride < s.D || s.stride > ((int64_t)1 << 31)) return GDN_ERR_SHAPE;
+    if ((!value_index && s.n > s.value_rows) || (!held_index && s.n > s.held_rows)) return GDN_ERR_SHAPE;
+    if (s.n > kMaxGrid || gdn::quant_grid(s.n, s.D) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (!values) return GDN_ERR_NULL;
+    const int st = check_held(held, true);
+    if (st != GDN_OK) return st;
+    if (misaligned(s.dtype, values) || misaligned(GDN_F32, value_index, held_index)) return GDN_ERR_ALIGN;
+    const gdn::QuantParams p{values, held_of(*held), value_index, held_index, s.n, s.D, s.stride, s.value_rows,
+                             s.held_rows};
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_quant(p, s.dtype, s.bits, back, (hipStream_t)stream, prof);
+    });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
 }  // namespace
 
 extern "C" {
@@ -819,6 +923,142 @@ int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, 
     p.part = (float *)workspace;
     const hipError_t err = with_profiler(
         [&](gdn::Profiler *prof) { return gdn::launch_norm_bwd(p, false, shape->dtype, (hipStream_t)stream, prof); });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward) {
+    if (!shape || shape->B < 0 || shape->T < 0 || shape->D <= 0 || shape->D > (1 << 26)) return 0;
+    if (gdn::elem_bytes(shape->dtype) == 0 || gdn::elem_bytes(shape->gate_dtype) == 0) return 0;
+    const int64_t tokens = (int64_t)shape->B * shape->T;
+    if (tokens > INT_MAX - 64) return 0;
+    return gdn::scan_workspace_bytes(tokens, shape->D, shape->dtype, scan_gate_f32(*shape), backward != 0);
+}
+
+int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state,
+                 const int32_t *cu_seqlens, void *out, float *final_state, const gdn_scan_shape *shape,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    return scan_fwd(x, g, beta, initial_state, nullptr, cu_seqlens, out, final_state, shape, workspace,
+                    workspace_bytes, stream);
+}
+
+int gdn_scan_fwd_pool(const void *x, const void *g, const void *beta, const gdn_state_pool *pool,
+                      const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    if (!pool) return GDN_ERR_NULL;
+    return scan_fwd(x, g, beta, nullptr, pool, cu_seqlens, out, nullptr, shape, workspace, workspace_bytes, stream);
+}
+
+int gdn_scan_steps(const void *x, const void *g, const void *beta, const gdn_step_pool *pool,
+                   const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *stream) {
+    int st = check_scan(shape, cu_seqlens, beta != nullptr);
+    if (st != GDN_OK) return st;
+    const gdn_scan_shape &s = *shape;
+    if (!pool) return GDN_ERR_NULL;
+    if (gdn::elem_bytes(pool->dtype) == 0) return GDN_ERR_DTYPE;
+    if ((int64_t)s.B * s.T == 0) return GDN_OK;
+    if (!x || !g || !out) return GDN_ERR_NULL;
+    if (misaligned(s.dtype, x, out) || misaligned(s.gate_dtype, g, beta)) return GDN_ERR_ALIGN;
+    st = check_slots(*pool, gdn::elem_bytes(pool->dtype));
+    if (st != GDN_OK) return st;
+    gdn::ScanParams p = scan_params(s, x, g, beta, cu_seqlens);
+    p.slots = slots_of(*pool);
+    p.state_bf16 = pool->dtype == GDN_BF16;
+    p.y = out;
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_scan_steps(p, s.dtype, scan_gate_f32(s), (hipStream_t)stream, prof);
+    });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_scan_bwd(const void *x, const void *g, const void *beta, const void *y, const gdn_held *x8,
+                 const gdn_held *y8, const void *dout, const float *dht, const float *initial_state,
+                 const int32_t *cu_seqlens, void *dx, void *dg, void *dbeta, float *dinitial,
+                 const gdn_scan_shape *shape, void *workspace, size_t workspace_bytes, void *stream) {
+    int st = check_scan(shape, cu_seqlens, beta != nullptr);
+    if (st != GDN_OK) return st;
+    const gdn_scan_shape &s = *shape;
+    const bool any = (int64_t)s.B * s.T > 0;
+    if (any && (!g || !dout || !dx || !dg || (!y8 && !y) || (beta && (!dbeta || (y8 ? !x8 : !x))) || (!beta && dbeta)))
+        return GDN_ERR_NULL;
+    if (y8) st = check_held(y8, any);
+    if (st == GDN_OK && y8 && beta) st = check_held(x8, any);
+    if (st != GDN_OK) return st;
+    if (misaligned(s.dtype, x, y, dout, dx) || misaligned(s.gate_dtype, g, beta, dg, dbeta) ||
+        misaligned(GDN_F32, dht, initial_state, dinitial))
+        return GDN_ERR_ALIGN;
+    st = check_scan_ws(s, true, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    gdn::ScanParams p = scan_params(s, x, g, beta, cu_seqlens);
+    p.y = const_cast<void *>(y);
+    if (y8) p.y8 = held_of(*y8);
+    if (y8 && beta) p.x8 = held_of(*x8);
+    p.dy = dout;
+    p.dht = dht;
+    p.initial = initial_state;
+    p.dx = dx;
+    p.dg = dg;
+    p.dbeta = dbeta;
+    p.dinitial = dinitial;
+    p.ws = workspace;
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_scan_bwd(p, s.dtype, scan_gate_f32(s), (hipStream_t)stream, prof);
+    });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_hold(const void *values, const int32_t *value_index, const gdn_held *held, const int32_t *held_index,
+             const gdn_held_shape *shape, void *stream) {
+    return hold(const_cast<void *>(values), value_index, held, held_index, shape, false, stream);
+}
+
+int gdn_restore(const gdn_held *held, const int32_t *held_index, void *values, const int32_t *value_index,
+                const gdn_held_shape *shape, void *stream) {
+    return hold(values, value_index, held, held_index, shape, true, stream);
+}
+
+int gdn_gated_norm_hold(const void *x, const void *z, const void *weight, float eps, void *out,
+                        const gdn_held *x8, const gdn_held *z8, const gdn_norm_shape *shape, void *stream) {
+    int st = check_gated(shape, weight);
+    if (st != GDN_OK) return st;
+    const bool any = shape->rows > 0;
+    st = check_held(x8, any);
+    if (st == GDN_OK) st = check_held(z8, any);
+    if (st != GDN_OK) return st;
+    if (!any) return GDN_OK;
+    if (!x || !z || !out) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, x, z, out)) return GDN_ERR_ALIGN;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.x = x;
+    p.z = z;
+    p.y = out;
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_norm_held(p, held_of(*x8), held_of(*z8), shape->dtype, (hipStream_t)stream, prof);
+    });
+    return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_gated_norm_hold_bwd(const gdn_held *x8, const gdn_held *z8, const void *weight, float eps, const void *dout,
+                            void *dx, void *dz, float *dweight, const gdn_norm_shape *shape, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    int st = check_gated(shape, weight);
+    if (st != GDN_OK) return st;
+    const bool any = shape->rows > 0;
+    st = check_held(x8, any);
+    if (st == GDN_OK) st = check_held(z8, any);
+    if (st != GDN_OK) return st;
+    if (any && (!dout || !dx || !dz)) return GDN_ERR_NULL;
+    if (misaligned(shape->dtype, dout, dx, dz)) return GDN_ERR_ALIGN;
+    st = check_norm_ws(*shape, dweight, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    gdn::NormParams p = norm_params(*shape, weight, eps);
+    p.dy = dout;
+    p.dx = dx;
+    p.dz = dz;
+    p.dweight = dweight;
+    p.part = (float *)workspace;
+    const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
+        return gdn::launch_norm_held_bwd(p, held_of(*x8), held_of(*z8), shape->dtype, (hipStream_t)stream, prof);
+    });
     return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

@@ -1,7 +1,8 @@
 // Internal interface of the operators around the delta rule in a GDN layer:
 // the recurrent steps over several tokens (gdn_steps.hip), the short causal
-// convolution (gdn_conv.hip) and the RMS norms (gdn_norm.hip).  Not part of the
-// public ABI.
+// convolution (gdn_conv.hip), the RMS norms (gdn_norm.hip, gdn_norm_held.hip), the
+// gated linear recurrence (gdn_scan.hip) and values held in 8 and 4 bits
+// (gdn_quant.hip).  Not part of the public ABI.
 #pragma once
 
 #include "gdn_internal.h"
@@ -10,7 +11,8 @@ namespace gdn {
 
 // Kernel kinds of the timing hook, after those of gdn_internal.h.
 enum LayerKernelKind { kStepsKernel = kNumKernelKinds, kConvKernel, kConvUpdateKernel, kConvBwdKernel, kNormKernel,
-                       kNormBwdKernel, kColumnSumKernel, kNumAllKinds };
+                       kNormBwdKernel, kColumnSumKernel, kScanKernel, kScanStepsKernel, kScanBwdKernel,
+                       kQuantKernel, kDequantKernel, kNumAllKinds };
 const char *layer_kernel_name(int kind);
 
 // Slots of a pool that a few-token step reads and writes: sequence n starts
@@ -89,6 +91,59 @@ constexpr int kGatedMaxD = 1024;     // one row in the registers of one wave
 hipError_t launch_norm(const NormParams &p, bool gated, int dtype, hipStream_t stream, Profiler *prof);
 size_t norm_bwd_workspace_bytes(int64_t rows, int D);
 hipError_t launch_norm_bwd(const NormParams &p, bool gated, int dtype, hipStream_t stream, Profiler *prof);
+
+// Values held in 8 bits: codes [rows, D] and bf16 scales [rows, groups of 32].
+struct Held {
+    void *codes, *scales;
+};
+constexpr int kGroup = 32;           // elements of one scale
+
+// The gated norm that also writes its inputs in 8 bits (x8, z8), and its gradients
+// from those (x and z of p are not read).
+hipError_t launch_norm_held(const NormParams &p, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
+                            Profiler *prof);
+hipError_t launch_norm_held_bwd(const NormParams &p, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
+                                Profiler *prof);
+
+// Rows of D values <-> codes and scales.  Row i of n lies at row src[i] (i without
+// src) of its tensor and goes to row dst[i] (i); a row with an index outside
+// its tensor is skipped.
+struct QuantParams {
+    void *values;                    // [value_rows, D], rows stride elements apart
+    Held held;                       // [held_rows, D (8 bits) or (D + 1) / 2 bytes (4 bits)], [held_rows, groups]
+    const int32_t *value_index, *held_index;   // [n] or null
+    int64_t n, D, stride;
+    int value_rows, held_rows;
+};
+hipError_t launch_quant(const QuantParams &p, int dtype, int bits, bool back, hipStream_t stream, Profiler *prof);
+int64_t quant_grid(int64_t n, int64_t D);
+
+// The gated linear recurrence h_t = e^g_t h_(t-1) + beta_t x_t per channel.
+struct ScanParams {
+    const void *x, *g, *beta;        // [T_tot, D], rows x/g/beta_stride elements apart; beta may be null
+    int64_t x_stride, g_stride, beta_stride;
+    const void *initial;             // [N, D] fp32, or a pool when indices is set; may be null
+    void *final_state;               // the same, may be null, may be `initial`
+    const int32_t *indices;          // [N] slots of initial / final_state, or null
+    int pool_size;
+    int state_bf16;                  // type of a pool's slots
+    StepSlots slots;                 // few tokens per sequence
+    const int32_t *cu_seqlens;       // [N+1] or null
+    void *y;                         // [T_tot, D]; in the backward pass the forward's output (read)
+    Held x8, y8;                     // backward: x and y in 8 bits instead (y8.codes non-null)
+    const void *dy;                  // [T_tot, D]
+    const float *dht;                // [N, D] or null
+    void *dx, *dg, *dbeta;           // [T_tot, D]; dbeta null without beta
+    float *dinitial;                 // [N, D] or null
+    void *ws;                        // scan_workspace_bytes
+    int T, T_tot, D, N;
+};
+// gate_f32: g, beta and their gradients are fp32 (else the element type).
+size_t scan_workspace_bytes(int64_t T_tot, int D, int dtype, int gate_f32, bool backward);
+int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N);
+hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
+hipError_t launch_scan_bwd(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
+hipError_t launch_scan_steps(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
 
 // out[c] = sum over i < n of part[i * cols + c], in a fixed order (gdn_norm.hip).
 // With W > 0 the columns are W + 1 planes of D: planes 0 .. W-1 go to

@@ -22,29 +22,12 @@
 // bf16 take 110 us forward, 524,288 gated rows of 128 67, their gradients 111, those
 // of 16,383 rows of 4096 114: 5.9 to 6.1 TB/s.  Gradients of rows above 8192 spill (300
 // bytes a lane of the 1024): 4096 rows of 16,384 390 us, 1.7 TB/s, forward 96.
-#include "gdn_layer_device.h"
+#include "gdn_norm_device.h"
 
 namespace gdn {
 namespace {
 
 using namespace dev;
-
-constexpr int threads_of(int L) { return L <= 64 ? 256 : L; }
-
-// Sum over the L lanes of a group, in every lane of it.  red: two rows of 16
-// floats, used in turn so that one barrier a call is enough.
-template <int L> __device__ __forceinline__ float group_sum(float x, float (*red)[16], int turn) {
-#pragma unroll
-    for (int o = (L < 64 ? L : 64) / 2; o >= 1; o >>= 1) x += __shfl_xor(x, o);
-    if constexpr (L > 64) {
-        if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = x;
-        lds_barrier();
-        x = 0.f;
-#pragma unroll
-        for (int w = 0; w < L / 64; ++w) x += red[turn][w];
-    }
-    return x;
-}
 
 // Elements [at, at + n) of a row: a lane's vector.  The last one of a row of an
 // odd length ends with the row and begins `dup` elements inside its neighbour's,
@@ -301,44 +284,6 @@ __global__ void __launch_bounds__(CL * RL) column_sum_kernel(const float *__rest
     }
 }
 
-// Lanes of a row's group and vectors a lane for D elements.
-struct Split {
-    int L, NV;
-};
-Split split_of(int D) {
-    if (D <= 64) return {8, 1};
-    if (D <= 128) return {16, 1};
-    if (D <= 256) return {32, 1};
-    if (D <= 512) return {64, 1};
-    if (D <= 1024) return {64, 2};
-    if (D <= 2048) return {256, 1};
-    if (D <= 4096) return {512, 1};
-    if (D <= 8192) return {1024, 1};
-    return {1024, 2};
-}
-
-// Workgroups of `waves` waves in all, fewer for few rows.
-int blocks_of(int64_t rows, int D, int waves) {
-    const int L = split_of(D).L, t = threads_of(L), gpb = t / L;
-    const int64_t b = (rows + gpb - 1) / gpb, most = waves * 64 / t;
-    return (int)(b < most ? b : most);
-}
-// Forward: many short-lived waves (16,384 x 32 gated rows of 128: 32768 waves 68
-// us, 8192 74), but few of the 1024-thread workgroups (8192 rows of 8192: 4096
-// waves 94 us, 8192 97, 32768 100).
-int norm_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L == 1024 ? 4096 : 32768); }
-// Backward: two waves a SIMD, walking the rows with the next one loading, keep the
-// memory busiest and leave the fewest partial sums (16,383 rows of 4096: 2048
-// waves 114 us, 4096 125, 1024 157; gated rows of 128 111, 125 and 135), and every
-// CU has a workgroup.
-int norm_bwd_blocks(int64_t rows, int D) { return blocks_of(rows, D, split_of(D).L == 1024 ? 4096 : 2048); }
-
-// Passes over more than the 256 MiB of the last cache are streamed past it: 16,384
-// rows of 5120 forward 110 against 122 us (with plain loads 117), 16,383 of 4096
-// backward 114 against 127; 16,384 x 32 gated rows of 128 forward 67 against 77,
-// backward 111 against 129.  Smaller outputs stay there for their reader.
-bool streams(const NormParams &p, size_t elem, int tensors) { return (size_t)p.rows * p.D * elem * tensors > (256u << 20); }
-
 template <typename E, int L, int NV, bool GATED>
 void launch_cfg(const NormParams &p, bool bwd, hipStream_t st) {
     if (bwd) {
@@ -426,6 +371,11 @@ const char *layer_kernel_name(int kind) {
         case kNormKernel: return "norm_kernel";
         case kNormBwdKernel: return "norm_bwd_kernel";
         case kColumnSumKernel: return "column_sum_kernel";
+        case kScanKernel: return "scan_kernel";
+        case kScanStepsKernel: return "scan_steps_kernel";
+        case kScanBwdKernel: return "scan_bwd_kernel";
+        case kQuantKernel: return "quant_kernel";
+        case kDequantKernel: return "dequant_kernel";
         default: return "unknown";
     }
 }

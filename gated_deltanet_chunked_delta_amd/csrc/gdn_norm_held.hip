@@ -1,0 +1,236 @@
+// The gated RMS norm of a GDN layer that keeps its inputs in 8 bits for gfx950:
+//   y = x r w silu(z),   r = (mean of squares + eps)^-1/2
+// forward with the codes of x and z written beside y in the one pass that reads
+// them, backward from the codes.  The arithmetic is that of gdn_norm.hip, on the
+// values that the codes stand for; the format that of gdn_quant_device.h.
+//
+// Bound by HBM.  Against the norm that keeps x and z as they are the forward pass
+// writes two bytes more an element (bf16: 8.1 instead of 6) and the backward pass
+// reads two less (8.1 instead of 10); what lives from one to the other is halved.
+#include "gdn_norm_device.h"
+#include "gdn_quant_device.h"
+
+namespace gdn {
+namespace {
+
+using namespace dev;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+
+// A lane's vectors are the row's eights in order, so that four neighbours make a
+// group of the format; the last one of a row may be short.
+template <typename E, int L, int NV>
+__global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, Held x8, Held z8) {
+    typedef Raw8<E> R;
+    typedef typename R::T V;
+    constexpr int GPB = threads_of(L) / L;
+    __shared__ float red[2][16];
+    const int l = threadIdx.x % L;
+    const int64_t rows_a_turn = (int64_t)gridDim.x * GPB;
+    const E *__restrict__ x = (const E *)p.x, *__restrict__ z = (const E *)p.z;
+    E *__restrict__ y = (E *)p.y;
+    const int D = p.D, groups = (D + kGroup - 1) / kGroup;
+    const float inv = 1.f / (float)D;
+    float w[NV][8];
+    int cnt[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        cnt[i] = min(max(D - (i * L + l) * 8, 0), 8);
+        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], true, p.w_f32, w[i]);
+    }
+    V xa[NV], za[NV];
+    auto load = [&](int64_t row) {
+        const int64_t at = row * D;
+        const int64_t zat = p.heads == 1 ? row * p.z_stride
+                                         : (int64_t)((uint32_t)row / (uint32_t)p.heads) * p.z_stride +
+                                               (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            xa[i] = load_n<E>(x + at + (i * L + l) * 8, cnt[i], true);
+            za[i] = load_n<E>(z + zat + (i * L + l) * 8, cnt[i], true);
+        }
+    };
+    auto keep = [&](const float *v, const Held &to, int64_t row, int i) {
+        uint32_t high = 0, c[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) high = max(high, __float_as_uint(v[e]) & 0x7fffffffu);
+        high = max(high, (uint32_t)__shfl_xor((int)high, 1));
+        high = max(high, (uint32_t)__shfl_xor((int)high, 2));
+        const float s = held_scale<127>(high), si = held_inverse(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = held_code<E>(v[e], s, si);
+        const int col = (i * L + l) * 8;
+        const uint32_t a = pack4(c), b = pack4(c + 4);
+        uint8_t *dst = (uint8_t *)to.codes + row * D + col;
+        if (cnt[i] == 8)
+            *(u32x2u *)dst = u32x2u{a, b};
+        else
+            for (int e = 0; e < cnt[i]; ++e) dst[e] = (uint8_t)((e < 4 ? a : b) >> (8 * (e % 4)));
+        if (l % 4 == 0 && cnt[i] > 0) ((bf16 *)to.scales)[row * groups + col / kGroup] = (bf16)s;
+    };
+    int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
+    if (row < p.rows) load(row);
+    for (int turn = 0; row < p.rows; row += rows_a_turn, turn ^= 1) {
+        float h[NV][8], g[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[i][e] = R::get(xa[i], e);
+                g[i][e] = R::get(za[i], e);
+                ss = fmaf(h[i][e], h[i][e], ss);
+            }
+        if (row + rows_a_turn < p.rows) load(row + rows_a_turn);
+        const float r = rsqrtf(group_sum<L>(ss, red, turn) * inv + p.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            V o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) R::set(o, e, h[i][e] * r * w[i][e] * (g[i][e] * sigmoid_f(g[i][e])));
+            store_n<E>(y + row * D + (i * L + l) * 8, o, cnt[i], true);
+            keep(h[i], x8, row, i);
+            keep(g[i], z8, row, i);
+        }
+    }
+}
+
+template <typename E, int L, int NV>
+__global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {
+    typedef Raw8<E> R;
+    typedef typename R::T V;
+    constexpr int NT = threads_of(L), GPB = NT / L;
+    __shared__ float red[2][16];
+    __shared__ float red2[2][16];
+    __shared__ float acc[GPB][L * NV * 8];
+    const int l = threadIdx.x % L;
+    const int64_t rows_a_turn = (int64_t)gridDim.x * GPB;
+    const E *__restrict__ dy = (const E *)p.dy;
+    E *__restrict__ dx = (E *)p.dx, *__restrict__ dz = (E *)p.dz;
+    const int D = p.D, groups = (D + kGroup - 1) / kGroup;
+    const float inv = 1.f / (float)D;
+    float w[NV][8], dw[NV][8];
+    int cnt[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        cnt[i] = min(max(D - (i * L + l) * 8, 0), 8);
+        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], true, p.w_f32, w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+    }
+    auto fetch = [&](const Held &h, int64_t row, int i, u32x2 &codes, float &scale) {
+        const int col = (i * L + l) * 8;
+        const uint8_t *src = (const uint8_t *)h.codes + row * D + col;
+        codes = u32x2{0, 0};
+        scale = 0.f;
+        if (cnt[i] > 0) scale = (float)((const bf16 *)h.scales)[row * groups + col / kGroup];
+        if (cnt[i] == 8)
+            codes = *(const u32x2u *)src;
+        else
+            for (int e = 0; e < cnt[i]; ++e) codes[e / 4] |= (uint32_t)src[e] << (8 * (e % 4));
+    };
+    V da[NV];
+    u32x2 xc[NV], zc[NV];
+    float xs[NV], zs[NV];
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            da[i] = load_n<E>(dy + row * D + (i * L + l) * 8, cnt[i], true);
+            fetch(x8, row, i, xc[i], xs[i]);
+            fetch(z8, row, i, zc[i], zs[i]);
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
+    if (row < p.rows) load(row);
+    for (int turn = 0; row < p.rows; row += rows_a_turn, turn ^= 1) {
+        float h[NV][8], u[NV][8], g[NV][8];
+        float ss = 0.f, sh = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[i][e] = held_byte(xc[i][e / 4], e % 4) * xs[i];
+                g[i][e] = held_byte(zc[i][e / 4], e % 4) * zs[i];
+                u[i][e] = R::get(da[i], e);
+                ss = fmaf(h[i][e], h[i][e], ss);
+                sh = fmaf(u[i][e] * w[i][e] * (g[i][e] * sigmoid_f(g[i][e])), h[i][e], sh);
+            }
+        if (row + rows_a_turn < p.rows) load(row + rows_a_turn);
+        const float r = rsqrtf(group_sum<L>(ss, red, turn) * inv + p.eps);
+        const float c = group_sum<L>(sh, red2, turn) * r * inv;       // mean(n u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            V o, oz;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float nv = h[i][e] * r, s = sigmoid_f(g[i][e]);
+                const float dn = u[i][e] * (g[i][e] * s);             // dy silu(z)
+                dw[i][e] = fmaf(dn, nv, dw[i][e]);
+                R::set(oz, e, u[i][e] * nv * w[i][e] * (s * fmaf(g[i][e], 1.f - s, 1.f)));
+                R::set(o, e, r * (dn * w[i][e] - nv * c));
+            }
+            store_n<E>(dx + row * D + (i * L + l) * 8, o, cnt[i], true);
+            store_n<E>(dz + row * D + (i * L + l) * 8, oz, cnt[i], true);
+        }
+    }
+    // the workgroup's sums of dw: over its rows' lane groups in order
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[threadIdx.x / L][(i * L + l) * 8 + e] = dw[i][e];
+    __syncthreads();
+    float *part = p.part + (int64_t)blockIdx.x * D;
+    for (int c = threadIdx.x; c < D; c += NT) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < GPB; ++q) s += acc[q][c];
+        part[c] = s;
+    }
+}
+
+template <typename E, int L, int NV> void launch_cfg(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
+    if (bwd)
+        norm_held_bwd_kernel<E, L, NV><<<norm_bwd_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+    else
+        norm_held_kernel<E, L, NV><<<norm_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+}
+template <typename E> void launch_e(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
+    const Split s = split_of(p.D);
+    if (s.L == 8) return launch_cfg<E, 8, 1>(p, x8, z8, bwd, st);
+    if (s.L == 16) return launch_cfg<E, 16, 1>(p, x8, z8, bwd, st);
+    if (s.L == 32) return launch_cfg<E, 32, 1>(p, x8, z8, bwd, st);
+    if (s.NV == 1) return launch_cfg<E, 64, 1>(p, x8, z8, bwd, st);
+    launch_cfg<E, 64, 2>(p, x8, z8, bwd, st);
+}
+hipError_t launch_any(const NormParams &p, const Held &x8, const Held &z8, int dtype, bool bwd, hipStream_t st) {
+    if (dtype == 0)
+        launch_e<bf16>(p, x8, z8, bwd, st);
+    else
+        launch_e<float>(p, x8, z8, bwd, st);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_held(const NormParams &p, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
+                            Profiler *prof) {
+    if (p.rows == 0) return hipSuccess;
+    if (prof) prof->begin(kNormKernel, stream);
+    const hipError_t err = launch_any(p, x8, z8, dtype, false, stream);
+    if (prof) prof->end(kNormKernel, stream);
+    return err;
+}
+
+hipError_t launch_norm_held_bwd(const NormParams &p, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
+                                Profiler *prof) {
+    if (p.rows > 0) {
+        if (prof) prof->begin(kNormBwdKernel, stream);
+        const hipError_t err = launch_any(p, x8, z8, dtype, true, stream);
+        if (prof) prof->end(kNormBwdKernel, stream);
+        if (err != hipSuccess) return err;
+    }
+    return launch_column_sum(p.part, p.rows > 0 ? norm_bwd_blocks(p.rows, p.D) : 0, p.D, p.dweight, p.D, 0, nullptr,
+                             stream, prof);
+}
+
+}  // namespace gdn

@@ -639,6 +639,159 @@ int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, 
                      void *dx, void *dresidual, float *dweight,
                      const gdn_norm_shape *shape, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The gated linear recurrence: the elementwise relative of the delta rule, one
+ * state a channel.  Per sequence and channel
+ *
+ *   h_t = e^(g_t) h_(t-1) + beta_t x_t,   out_t = h_t
+ *
+ * with the gates of the delta rule: g <= 0 in log space, the lowest value of its
+ * type or -infinity for a channel that forgets everything, beta the write
+ * strength (gdn_gating makes both, for any number of channels).  States are fp32.
+ *
+ * Sizes.
+ *   B, T, N       as in gdn_shape (with cu_seqlens B = 1)
+ *   D             channels, at most 2^26
+ *   dtype         gdn_dtype of x and out
+ *   gate_dtype    of g and beta: dtype or GDN_F32
+ *   x_stride, g_stride, beta_stride  elements between the rows of x, g and beta, at
+ *                 least D and at most 2^31 (they may be parts of wider rows;
+ *                 beta_stride is ignored without beta) */
+typedef struct gdn_scan_shape {
+    int32_t B, T, D, N;
+    int32_t dtype, gate_dtype;
+    int64_t x_stride, g_stride, beta_stride;
+} gdn_scan_shape;
+
+/* Bytes of device workspace that gdn_scan_fwd and gdn_scan_fwd_pool (backward = 0)
+ * or gdn_scan_bwd need for these sizes: tokens are cut into tiles whose states are
+ * handed on through it.  0 where one tile holds all tokens, and for invalid sizes. */
+size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward);
+
+/* The recurrence over whole sequences.
+ *
+ *   x             [B, T, D]   dtype        read, rows x_stride apart
+ *   g             [B, T, D]   gate_dtype   read, rows g_stride apart
+ *   beta          [B, T, D]   gate_dtype   read, rows beta_stride apart; NULL = 1
+ *   initial_state [N, D]      fp32 or NULL read; NULL = zeros
+ *   cu_seqlens    as for gdn_chunk_fwd
+ *   out           [B, T, D]   dtype        written (every element)
+ *   final_state   [N, D]      fp32 or NULL written (an empty sequence's is its
+ *                 initial state); may alias initial_state exactly
+ *   workspace     gdn_scan_workspace_bytes bytes, 16-byte aligned
+ *                 (GDN_ERR_WORKSPACE); contents on entry are ignored
+ *
+ * Outputs must not overlap each other, the inputs (final_state aside) or the
+ * workspace.  Tensors are aligned to their element.  Arithmetic is fp32, out
+ * rounded once, and the result of a call does not depend on scheduling.  Returns
+ * GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a sequence, more than
+ * 2^31 - 65 of them, or too many for one launch), GDN_ERR_DTYPE,
+ * GDN_ERR_UNSUPPORTED (gate_dtype), GDN_ERR_ALIGN, GDN_ERR_WORKSPACE or
+ * GDN_ERR_LAUNCH. */
+int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state,
+                 const int32_t *cu_seqlens, void *out, float *final_state, const gdn_scan_shape *shape,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* gdn_scan_fwd with the states in a pool [pool_size, D], fp32 or bf16, in place, as
+ * gdn_chunk_fwd_pool has them: a slot outside the pool gives a sequence a zero
+ * start and stores nothing; read_initial = 0 starts all of them from zero. */
+int gdn_scan_fwd_pool(const void *x, const void *g, const void *beta, const gdn_state_pool *pool,
+                      const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* The recurrence over a few tokens per sequence, states in a pool [pool_size, D],
+ * fp32 or bf16 (aligned to their element): see gdn_step_pool.  A sequence's tokens
+ * are taken in order by one wave.  No workspace; out must not overlap any input or
+ * the pool. */
+int gdn_scan_steps(const void *x, const void *g, const void *beta, const gdn_step_pool *pool,
+                   const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *stream);
+
+/* Values held in 8 or 4 bits.  The values of a row are taken in groups of 32 (the
+ * last one may be shorter).  With top = 127 (8 bits) or 7 (4 bits) a group's scale s
+ * is the smallest bf16 number that has top * s >= the largest magnitude in it, and
+ * 0 where that is below 2^-100; a value's code is the integer nearest to value / s,
+ * ties to even, in [-top, top]; it stands for code * s.  A group that holds an
+ * infinity or a NaN has a NaN scale and stands for NaNs.
+ *
+ *   codes         [rows, D] int8, or [rows, (D + 1) / 2] bytes with element 2i in
+ *                 the low and 2i + 1 in the high half of byte i, two's complement
+ *   scales        [rows, (D + 31) / 32] bf16 */
+typedef struct gdn_held {
+    void *codes;
+    void *scales;
+} gdn_held;
+
+/* Rows of values to be held, or restored.
+ *   n             rows of the call
+ *   D             values of a row, at most 2^31 - 1
+ *   stride        elements between the rows of values, at least D, at most 2^31
+ *   value_rows, held_rows  rows of the two tensors; indices are checked against them
+ *   dtype         gdn_dtype of the values
+ *   bits          8 or 4 (GDN_ERR_UNSUPPORTED) */
+typedef struct gdn_held_shape {
+    int64_t n, D, stride;
+    int32_t value_rows, held_rows;
+    int32_t dtype, bits;
+} gdn_held_shape;
+
+/* Writes rows of values into a cache of codes and scales: row value_index[i] of
+ * values goes to row held_index[i] of held, i < n.  With a state pool's slots as
+ * rows (D = HV K V for the delta rule's, D (W-1) for the convolution's) this
+ * keeps a request's state, or one at a prefix's end, in 8.5 or 4.5 bits an element.
+ *
+ *   value_index, held_index  [n] int32 (device) or NULL for 0 .. n-1; a pair with an
+ *                 index outside its tensor is skipped.  Two pairs must not name the
+ *                 same row to be written.
+ *
+ * Values and scales are aligned to their element (GDN_ERR_ALIGN), codes need no
+ * alignment.  The tensors must not overlap.  Returns GDN_OK, GDN_ERR_NULL,
+ * GDN_ERR_SHAPE (also n above value_rows or held_rows without that side's index, or
+ * too many rows for one launch: 2^24 - 1 blocks of 2048 values), GDN_ERR_DTYPE,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
+int gdn_hold(const void *values, const int32_t *value_index, const gdn_held *held, const int32_t *held_index,
+             const gdn_held_shape *shape, void *stream);
+
+/* Reads them back: row held_index[i] of held goes to row value_index[i] of values,
+ * code * s rounded once to dtype. */
+int gdn_restore(const gdn_held *held, const int32_t *held_index, void *values, const int32_t *value_index,
+                const gdn_held_shape *shape, void *stream);
+
+/* Backward pass of gdn_scan_fwd.  With dh the gradient of the states,
+ *
+ *   dh_t = dout_t + e^(g_(t+1)) dh_(t+1)    (dht added at a sequence's last token)
+ *   dx_t = beta_t dh_t,   dbeta_t = x_t dh_t,   dg_t = e^(g_t) h_(t-1) dh_t,
+ *   dinitial = e^(g_1) dh_1
+ *
+ * where h_(t-1) is the forward's out_(t-1) as it was rounded, or the initial state.
+ *
+ *   g, beta, initial_state, cu_seqlens, shape  as in the forward call
+ *   x             as in the forward call; NULL without beta (it is not needed)
+ *   y             [B, T, D]   dtype        read: the forward's out, contiguous
+ *   x8, y8        NULL, or x and y held in 8 bits (D as in shape; contiguous rows),
+ *                 read instead of x and y: both with beta, y8 alone without
+ *   dout          [B, T, D]   dtype        read
+ *   dht           [N, D]      fp32 or NULL read: gradient of final_state
+ *   dx            [B, T, D]   dtype        written
+ *   dg, dbeta     [B, T, D]   gate_dtype   written; dbeta NULL exactly without beta
+ *   dinitial      [N, D]      fp32 or NULL written
+ *   workspace     gdn_scan_workspace_bytes(shape, 1) bytes
+ *
+ * Outputs are contiguous; otherwise as for gdn_scan_fwd. */
+int gdn_scan_bwd(const void *x, const void *g, const void *beta, const void *y, const gdn_held *x8,
+                 const gdn_held *y8, const void *dout, const float *dht, const float *initial_state,
+                 const int32_t *cu_seqlens, void *dx, void *dg, void *dbeta, float *dinitial,
+                 const gdn_scan_shape *shape, void *workspace, size_t workspace_bytes, void *stream);
+
+/* gdn_gated_norm that also keeps its inputs in 8 bits for the backward pass, in the
+ * pass that reads them: x8 and z8 are written, [rows, D] codes and their scales. */
+int gdn_gated_norm_hold(const void *x, const void *z, const void *weight, float eps, void *out,
+                        const gdn_held *x8, const gdn_held *z8, const gdn_norm_shape *shape, void *stream);
+
+/* gdn_gated_norm_bwd at the values that x8 and z8 stand for.  shape: heads = 1 and
+ * z_stride = D do (z is not read).  Otherwise as for gdn_gated_norm_bwd. */
+int gdn_gated_norm_hold_bwd(const gdn_held *x8, const gdn_held *z8, const void *weight, float eps, const void *dout,
+                            void *dx, void *dz, float *dweight, const gdn_norm_shape *shape, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Kernel timing hook, for measurement.  While enabled, every call of the
  * entry points above records HIP events on its stream just before
  * and just after each kernel it enqueues (events are created on first use and
