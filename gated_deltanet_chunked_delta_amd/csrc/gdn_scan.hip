@@ -6,6 +6,11 @@
 // with h_(t-1) the forward's y_(t-1) as it was rounded, or the initial state.
 #include <algorithm>
 
+// Products and sums are fused where fmaf says so and nowhere else: two lanes that
+// share a channel (see lane_of) compute it at different places of their vectors and
+// have to get the same bits.
+#pragma clang fp contract(off)
+
 #include "gdn_quant_device.h"
 
 namespace gdn {
@@ -13,22 +18,23 @@ namespace {
 
 using namespace dev;
 
-// e^g for g <= 0 within 1.05 ulp, and 0.51 near 0: n = the integer nearest to
-// g / ln 2, r = g - n ln 2 in two parts, e^r = 1 + r + r^2 p(r) with p of degree 4
-// interpolating at Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2).  The hardware
-// exponential is off by an ulp of e^g however small g is, which a channel with
-// gates near 0 sums over all the tokens that it remembers.
+// e^g for g <= 0, with a relative error of at most 0.62 2^-24 down to -0.1, 1.3 2^-24
+// to -5 and 5.1 2^-24 to -87, and 0 below: n = the integer
+// nearest to g / ln 2, r = g - n ln 2, e^r = 1 + r + r^2 p(r) with p of degree 4
+// interpolating at Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n added to the
+// exponent.  The sum g / ln 2 + 1.5 2^23 has n in its low bits.  11 instructions; the
+// hardware exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on
+// average, which a channel sums over all the tokens that it remembers.
 __device__ __forceinline__ float decay(float g) {
-    g = g < -104.f ? -104.f : g;                       // e^-104 is below the smallest subnormal
-    const float n = rintf(g * 1.4426950408889634f);
-    float r = fmaf(n, -0.693145751953125f, g);
-    r = fmaf(n, -1.428606765330187e-06f, r);
+    const float t = fmaf(g, 1.4426950408889634f, kRoundBias);
+    const float r = fmaf(t - kRoundBias, -0.6931471805599453f, g);
     float q = fmaf(r, 0.0013926184f, 0.008363179f);
     q = fmaf(r, q, 0.041666556f);
     q = fmaf(r, q, 0.16666576f);
     q = fmaf(r, q, 0.5f);
-    q = fmaf(r * r, q, r);
-    return ldexpf(1.f + q, (int)n);
+    q = fmaf(r, q, 1.f);
+    q = fmaf(r, q, 1.f);
+    return g < -87.f ? 0.f : __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));   // NaN for a NaN
 }
 
 // One element as Raw has four and eight.
@@ -55,11 +61,12 @@ __device__ __forceinline__ void store_state(void *s, int64_t at, int b16, float 
 
 // ---------------------------------------------------------------------------
 // Tiles.  The tokens of all sequences lie on one axis, which is cut into tiles of
-// W * S tokens; a workgroup takes one tile of up to 64 * VC channels, every wave S
-// of its tokens, every lane VC channels.  All of it is loaded once, into registers;
-// what a wave's tokens do to a state is h -> A h + b, and such maps compose.
+// W * S tokens; a workgroup of W waves takes one tile of up to 64 * VC channels,
+// every wave S of its tokens, every lane VC channels.  All of it is loaded once,
+// into registers; what a wave's tokens do to a state is h -> A h + b, and such maps
+// compose.  The backward pass is the same with tiles, waves and tokens in reverse.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 8, kGroupTiles = 8;
+constexpr int kGroupTiles = 8, kBlockGroups = 8;   // tiles of a group, groups of a block
 
 // Channels of a lane.  The vectors of VC channels are shared out evenly among the
 // column blocks; the last one of an odd row ends with it and overlaps its neighbour,
@@ -75,17 +82,25 @@ template <int VC> __device__ __forceinline__ Lane lane_of(int D, int ncb, int cb
 }
 template <int VC> __host__ __device__ __forceinline__ int column_blocks(int D) { return ((D + VC - 1) / VC + 63) / 64; }
 
-// Workspace: a counter (16 bytes), then a word a tile and channel, what the tile does
-// to a state, then a word a group of tiles and channel, the state before the group.
+// Workspace: a counter (16 bytes), then words, a channel of a column block each: what a
+// tile does to a state, for all tiles; what a group does; the state before a block
+// of groups.  A tile's words lie in the order of its lanes' vectors, so that 64 lanes
+// move 512 bytes at a time.
 struct Handed {
-    uint32_t *counter;
-    unsigned long long *maps, *states;
+    unsigned long long *tiles, *groups, *states;
+    int64_t row;                                       // words of one tile, all column blocks
 };
-__host__ __device__ __forceinline__ Handed handed_of(void *ws, int64_t tiles, int D) {
-    unsigned long long *w = (unsigned long long *)ws;
-    return {(uint32_t *)w, w + 2, w + 2 + tiles * D};
+__host__ __device__ __forceinline__ int64_t groups_of(int64_t tiles) { return (tiles + kGroupTiles - 1) / kGroupTiles; }
+__host__ __device__ __forceinline__ int64_t handed_words(int64_t tiles, int64_t row) {
+    const int64_t groups = groups_of(tiles);
+    return 2 + (tiles + groups + (groups + kBlockGroups - 1) / kBlockGroups) * row;
 }
-int64_t handed_words(int64_t tiles, int D) { return 2 + (tiles + (tiles + kGroupTiles - 1) / kGroupTiles) * D; }
+// The words of column block cb, this lane's first.
+template <int VC> __device__ __forceinline__ Handed handed_of(void *ws, int64_t tiles, int ncb, int cb, int lane) {
+    const int64_t row = (int64_t)ncb * VC * 64;
+    unsigned long long *w = (unsigned long long *)ws + 2 + cb * VC * 64 + lane;
+    return {w, w + tiles * row, w + (tiles + groups_of(tiles)) * row, row};
+}
 
 // A word carries its own flag, the sign of its upper half (decays are not negative),
 // so that it is handed on without a fence: one 64-bit store and loads that repeat
@@ -94,23 +109,21 @@ __device__ __forceinline__ void put(unsigned long long *w, float A, float h) {
     __hip_atomic_store(w, (unsigned long long)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(h),
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-template <int VC> __device__ __forceinline__ void await(const unsigned long long *w, float *A, float *h) {
+template <int VC> __device__ __forceinline__ void await(const unsigned long long *w, float2 (*to)[64]) {
     unsigned long long v[VC];
     for (;;) {
         bool all = true;
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            v[e] = __hip_atomic_load(w + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v[e] = __hip_atomic_load(w + e * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             all = all && (long long)v[e] < 0;
         }
         if (all) break;
         __builtin_amdgcn_s_sleep(1);
     }
 #pragma unroll
-    for (int e = 0; e < VC; ++e) {
-        A[e] = __uint_as_float((uint32_t)(v[e] >> 32) & 0x7fffffffu);
-        h[e] = __uint_as_float((uint32_t)v[e]);
-    }
+    for (int e = 0; e < VC; ++e)
+        to[e][0] = float2{__uint_as_float((uint32_t)(v[e] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v[e])};
 }
 
 __global__ void __launch_bounds__(256) clear_kernel(uint4 *w, int64_t n) {
@@ -147,7 +160,7 @@ __device__ __forceinline__ void find_sequences(Sequences<TT> &q, const ScanParam
             q.first = t0 / p.T;
             q.first_token = q.first * p.T;
         }
-        __syncthreads();
+        lds_barrier();
         return;
     }
     for (int i = tid; i <= TT; i += NT) q.start[i] = -1;
@@ -156,22 +169,22 @@ __device__ __forceinline__ void find_sequences(Sequences<TT> &q, const ScanParam
         q.first = n0;
         q.first_token = cu_at(p.cu_seqlens, n0, p.T_tot);
     }
-    __syncthreads();
+    lds_barrier();
     for (int n = n0 + tid; n < p.N; n += NT) {
         const int at = cu_at(p.cu_seqlens, n, p.T_tot) - t0;
         if (at > TT) break;
         if (at >= 0) atomicMax(&q.start[at], n);
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 // Rows of sequences without tokens, shared out over the tiles: the final state is the
 // initial one.
-template <int VC>
+template <int VC, int W>
 __device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, int tiles, int c, bool live) {
     if (!p.final_state || (p.indices && p.initial) || !live) return;   // a pool's slots keep what they hold
     const int lo = (int)((int64_t)p.N * tile / tiles), hi = (int)((int64_t)p.N * (tile + 1) / tiles);
-    for (int n = lo + (threadIdx.x >> 6); n < hi; n += kWaves) {
+    for (int n = lo + (threadIdx.x >> 6); n < hi; n += W) {
         int t0, t1;
         seq_range(p.cu_seqlens, n, p.T, p.T_tot, t0, t1);
         if (t0 != t1) continue;
@@ -186,29 +199,152 @@ __device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, i
     }
 }
 
-template <typename E, typename G, bool BETA, int VC, int S>
-__global__ void __launch_bounds__(kWaves * 64) scan_kernel(ScanParams p, int ncb, int tiles) {
-    constexpr int NT = kWaves * 64, TT = kWaves * S;
+// Sequence of the token before token i of the tile (of the tile's first where i = 0).
+template <int TT> __device__ __forceinline__ int sequence_before(const Sequences<TT> &q, int i, int lane) {
+    int n = q.first;
+    for (int j = lane; j < i; j += 64) n = max(n, q.start[j]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) n = max(n, __shfl_xor(n, o));
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Tiles are taken in the order of a counter, so that whatever tile a workgroup waits
+// for is with a workgroup that runs already; as each hands its map on before it
+// waits, and the earliest one waits for none, every wait ends.
+__device__ __forceinline__ int next_tile(void *ws, int tiles, int *ticket) {
+    if (tiles == 1) return blockIdx.x;
+    if (threadIdx.x == 0) *ticket = (int)atomicAdd((uint32_t *)ws, 1u);
+    lds_barrier();
+    return __builtin_amdgcn_readfirstlane(*ticket);
+}
+
+template <int VC, int W> struct Exchange {
+    float2 maps[W][VC][64];                            // what each wave's tokens do to a state
+    float2 before[kGroupTiles + kBlockGroups - 1][VC][64];   // tiles and groups before this tile, the state before them
+    int cut[W];                                        // a state begins anew in the wave's tokens
+};
+// Maps lo .. hi - 1 of those that a tile waits for, one a wave: nt of tiles from `from`
+// on, ng of groups from gfrom on, the state before the block.
+template <int VC, int W>
+__device__ __forceinline__ void fetch(Exchange<VC, W> &x, const Handed &hand, int lane, int rank, int lo, int hi, int from,
+                                      int nt, int gfrom, int ng, int block) {
+    for (int k = lo + rank; k < hi; k += W) {
+        const unsigned long long *src = k < nt        ? hand.tiles + (from + k) * hand.row
+                                        : k < nt + ng ? hand.groups + (gfrom + k - nt) * hand.row
+                                                      : hand.states + block * hand.row;
+        await<VC>(src, (float2 (*)[64])&x.before[k][0][lane]);
+    }
+}
+// The state that comes into a wave's tokens.  rank: the wave's place in its tile, tile:
+// the tile's place in the order of the pass; A, b: the wave's map, fresh: whether a
+// state begins anew in it (its map is then b alone); waits: whether a state comes
+// into the tile, since: the place of the tile where it began.
+//
+// It is the state before the block of 64 tiles, then the maps of the block's groups
+// of 8 tiles before this one, then those of the tiles before this one in its group:
+// an order that depends on the sizes alone.  The last tile of a group hands on the
+// group's map, the last one of a block the state.  A state handed on from one
+// workgroup to another takes 2.8 us (a store, a load that meets it, the sum between);
+// with one level, from group to group, 131,072 tokens of 256 channels took 700 us.
+template <int VC, int W>
+__device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand, int lane, int rank, int tile, int tiles,
+                                         bool waits, int since, bool fresh, const float *A, const float *b, float *h) {
+#pragma unroll
+    for (int e = 0; e < VC; ++e) x.maps[rank][e][lane] = float2{A[e], b[e]};
+    if (lane == 0) x.cut[rank] = fresh;
+    lds_barrier();
+    bool own = false;                                  // the state began in the tile, before the wave
+    float Ae[VC], he[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e) {
+        Ae[e] = 1.f;
+        he[e] = 0.f;
+    }
+    for (int k = 0; k < rank; ++k) {
+        const bool anew = x.cut[k] != 0;
+        own = own || anew;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            const float2 m = x.maps[k][e][lane];
+            he[e] = anew ? m.y : fmaf(m.x, he[e], m.y);
+            Ae[e] *= m.x;
+        }
+    }
+    const bool last = rank == W - 1;                   // the wave whose end is the tile's
+    if (tiles > 1 && last) {
+#pragma unroll
+        for (int e = 0; e < VC; ++e)
+            put(hand.tiles + tile * hand.row + e * 64, Ae[e] * A[e], fresh ? b[e] : fmaf(A[e], he[e], b[e]));
+    }
+    const int group = tile / kGroupTiles, base = group * kGroupTiles, block = group / kBlockGroups;
+    const int from = max(base, since), nt = waits ? tile - from : 0;
+    const int gfrom = max(block * kBlockGroups, since / kGroupTiles), ng = waits && since < base ? group - gfrom : 0;
+    const bool further = waits && since < block * kBlockGroups * kGroupTiles;
+    const bool ends_group = tile % kGroupTiles == kGroupTiles - 1 && tile + 1 < tiles;
+    const int all = nt + ng + (further ? 1 : 0);
+    float At[VC], ht[VC], hin[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e) {
+        At[e] = 1.f;
+        ht[e] = hin[e] = 0.f;
+    }
+    if (waits) {
+        fetch<VC, W>(x, hand, lane, rank, 0, ends_group ? nt : all, from, nt, gfrom, ng, block);
+        lds_barrier();
+        for (int k = 0; k < nt; ++k)
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                const float2 m = x.before[k][e][lane];
+                ht[e] = since == from + k ? m.y : fmaf(m.x, ht[e], m.y);
+                At[e] *= m.x;
+            }
+    }
+    if (ends_group && last) {
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            const float T = Ae[e] * A[e], v = fresh ? b[e] : fmaf(A[e], he[e], b[e]);
+            put(hand.groups + group * hand.row + e * 64, At[e] * T, fresh || own ? v : fmaf(T, ht[e], v));
+        }
+    }
+    if (waits) {
+        if (ends_group) {
+            fetch<VC, W>(x, hand, lane, rank, nt, all, from, nt, gfrom, ng, block);
+            lds_barrier();
+        }
+        if (further)
+#pragma unroll
+            for (int e = 0; e < VC; ++e) hin[e] = x.before[nt + ng][e][lane].y;
+        for (int k = 0; k < ng; ++k)
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                const float2 m = x.before[nt + k][e][lane];
+                hin[e] = since / kGroupTiles == gfrom + k ? m.y : fmaf(m.x, hin[e], m.y);
+            }
+#pragma unroll
+        for (int e = 0; e < VC; ++e) hin[e] = since < base ? fmaf(At[e], hin[e], ht[e]) : ht[e];
+    }
+#pragma unroll
+    for (int e = 0; e < VC; ++e) h[e] = own ? he[e] : fmaf(Ae[e], hin[e], he[e]);
+    if (ends_group && group % kBlockGroups == kBlockGroups - 1 && last) {
+#pragma unroll
+        for (int e = 0; e < VC; ++e)
+            put(hand.states + (block + 1) * hand.row + e * 64, 0.f, fresh ? b[e] : fmaf(A[e], h[e], b[e]));
+    }
+}
+
+template <typename E, typename G, bool BETA, int VC, int W, int S>
+__global__ void __launch_bounds__(W * 64) scan_kernel(ScanParams p, int ncb, int tiles) {
+    constexpr int NT = W * 64, TT = W * S;
     __shared__ Sequences<TT> q;
-    __shared__ float2 maps[kWaves][VC][64];            // what each wave's tokens do to a state
-    __shared__ float2 before[kGroupTiles][VC][64];     // the tiles of the group before this one
-    __shared__ float into[VC][64];                     // the state before the group
-    __shared__ int cut[kWaves];                        // the last sequence that begins in a wave's tokens, or -1
+    __shared__ Exchange<VC, W> x;
     __shared__ int ticket;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Handed hand = handed_of(p.ws, tiles, p.D);
-    // Tiles are taken in the order of a counter, so that whatever tile a workgroup
-    // waits for is with a workgroup that runs already; as each hands its map on
-    // before it waits, and the earliest one waits for none, every wait ends.
-    if (tiles > 1) {
-        if (threadIdx.x == 0) ticket = (int)atomicAdd(hand.counter, 1u);
-        __syncthreads();
-    }
-    const int id = tiles > 1 ? __builtin_amdgcn_readfirstlane(ticket) : blockIdx.x;
-    const int tile = id / ncb, cb = id % ncb, t0 = tile * TT;
-    const Lane ln = lane_of<VC>(p.D, ncb, cb, lane);
+    const int id = next_tile(p.ws, tiles, &ticket);
+    const Handed hand = handed_of<VC>(p.ws, tiles, ncb, id % ncb, lane);
+    const int tile = id / ncb, t0 = tile * TT;
+    const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
     const int t_end = p.cu_seqlens ? cu_at(p.cu_seqlens, p.N, p.T_tot) : p.T_tot;
-    empty_sequences<VC>(p, tile, tiles, ln.c, ln.live);
+    empty_sequences<VC, W>(p, tile, tiles, ln.c, ln.live);
     if (t0 >= t_end) return;
     const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the wave's tokens
 
@@ -218,17 +354,17 @@ __global__ void __launch_bounds__(kWaves * 64) scan_kernel(ScanParams p, int ncb
     {
         typename RE::T xr[S];
         typename RG::T gr[S], br[S];
-        const E *x = (const E *)p.x + (int64_t)tw * p.x_stride;
-        const G *g = (const G *)p.g + (int64_t)tw * p.g_stride, *b = (const G *)p.beta + (int64_t)tw * p.beta_stride;
+        const E *xp = (const E *)p.x + (int64_t)tw * p.x_stride;
+        const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             xr[s] = RE::zero();
             gr[s] = RG::zero();                        // a = 1, u = 0: the state stays
             if (BETA) br[s] = RG::zero();
             if (s < nv && ln.live) {
-                xr[s] = RE::load(x + s * p.x_stride + ln.c);
-                gr[s] = RG::load(g + s * p.g_stride + ln.c);
-                if (BETA) br[s] = RG::load(b + s * p.beta_stride + ln.c);
+                xr[s] = RE::load(xp + s * p.x_stride + ln.c);
+                gr[s] = RG::load(gp + s * p.g_stride + ln.c);
+                if (BETA) br[s] = RG::load(bp + s * p.beta_stride + ln.c);
             }
         }
         find_sequences<TT, NT>(q, p, t0, t_end);
@@ -242,118 +378,45 @@ __global__ void __launch_bounds__(kWaves * 64) scan_kernel(ScanParams p, int ncb
             }
     }
     // sequences that begin at, or end with, the wave's tokens
-    const bool is = lane < S && lane < nv;
+    const bool is = lane < nv;
     const int at = w * S + min(lane, S - 1);
     const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
     const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
-    // The state that a sequence starts from takes the place of the one that came in:
-    // it is read once, before this tile's map is handed on, since its buffer may be
-    // the final state's.
-    auto initial = [&](int n, float *h) {
-        int64_t from = (int64_t)n * p.D + ln.c;
-        bool has = p.initial != nullptr && ln.live;
-        if (p.indices) {
-            const int slot = p.indices[n];
-            has = has && slot >= 0 && slot < p.pool_size;
-            from = (int64_t)slot * p.D + ln.c;
-        }
-#pragma unroll
-        for (int e = 0; e < VC; ++e) h[e] = has ? load_state(p.initial, from + e, p.state_bf16) : 0.f;
-    };
-    float A[VC], h[VC];
-    int last = -1;                                     // the last sequence that begins here
+    float A[VC], h[VC], b[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
         A[e] = 1.f;
-        h[e] = 0.f;
+        b[e] = 0.f;
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (starts >> s & 1) {
-            float h0[VC];
-            last = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
-            initial(last, h0);
+            // The state that the sequence starts from takes the place of the one that
+            // came in.  It is read once, before the tile's map is handed on: its
+            // buffer may be the final state's.
+            const int n = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+            int64_t from = (int64_t)n * p.D + ln.c;
+            bool has = p.initial != nullptr && ln.live;
+            if (p.indices) {
+                const int slot = p.indices[n];
+                has = has && slot >= 0 && slot < p.pool_size;
+                from = (int64_t)slot * p.D + ln.c;
+            }
 #pragma unroll
-            for (int e = 0; e < VC; ++e) h[e] = u[s][e] = fmaf(a[s][e], h0[e], u[s][e]);
+            for (int e = 0; e < VC; ++e) {
+                const float h0 = has ? load_state(p.initial, from + e, p.state_bf16) : 0.f;
+                b[e] = u[s][e] = fmaf(a[s][e], h0, u[s][e]);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < VC; ++e) h[e] = fmaf(a[s][e], h[e], u[s][e]);
+            for (int e = 0; e < VC; ++e) b[e] = fmaf(a[s][e], b[e], u[s][e]);
         }
 #pragma unroll
         for (int e = 0; e < VC; ++e) A[e] *= a[s][e];
     }
-#pragma unroll
-    for (int e = 0; e < VC; ++e) maps[w][e][lane] = float2{A[e], h[e]};
-    if (lane == 0) cut[w] = last;
-    __syncthreads();
-    // the tokens before this wave's in the tile; the last wave hands the tile's map on
-    int seq = q.first;                                 // sequence before the wave's first token
-    bool own = false;                                  // it began in the tile
-    float Ae[VC], he[VC];
-#pragma unroll
-    for (int e = 0; e < VC; ++e) {
-        Ae[e] = 1.f;
-        he[e] = 0.f;
-    }
-    for (int k = 0; k < w; ++k) {
-        const bool fresh = cut[k] >= 0;
-        own = own || fresh;
-        seq = max(seq, cut[k]);
-#pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            const float2 m = maps[k][e][lane];
-            he[e] = fresh ? m.y : fmaf(m.x, he[e], m.y);
-            Ae[e] *= m.x;
-        }
-    }
-    const int base = tile / kGroupTiles * kGroupTiles;
-    if (tiles > 1 && w == kWaves - 1 && ln.live) {
-#pragma unroll
-        for (int e = 0; e < VC; ++e)
-            put(hand.maps + (int64_t)tile * p.D + ln.c + e, Ae[e] * A[e], starts ? h[e] : fmaf(A[e], he[e], h[e]));
-    }
-    // the state that comes into the tile
-    const int since = q.first_token / TT;              // tile in which its first sequence begins
-    float hin[VC];
-#pragma unroll
-    for (int e = 0; e < VC; ++e) hin[e] = 0.f;
-    if (q.first_token < t0) {
-        const int from = max(base, since), n = tile - from;
-        if (w < n) {
-            float m[VC], b[VC];
-            if (ln.live) await<VC>(hand.maps + (int64_t)(from + w) * p.D + ln.c, m, b);
-#pragma unroll
-            for (int e = 0; e < VC; ++e) before[w][e][lane] = float2{m[e], b[e]};
-        }
-        if (since < base && w == kWaves - 1) {
-            float m[VC], b[VC];
-            if (ln.live) await<VC>(hand.states + (int64_t)(base / kGroupTiles) * p.D + ln.c, m, b);
-#pragma unroll
-            for (int e = 0; e < VC; ++e) into[e][lane] = b[e];
-        }
-        __syncthreads();
-        if (since < base)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) hin[e] = into[e][lane];
-        for (int k = 0; k < n; ++k)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                const float2 m = before[k][e][lane];
-                hin[e] = since == from + k ? m.y : fmaf(m.x, hin[e], m.y);
-            }
-    }
-#pragma unroll
-    for (int e = 0; e < VC; ++e) h[e] = own ? he[e] : fmaf(Ae[e], hin[e], he[e]);
-    if (tile % kGroupTiles == kGroupTiles - 1 && tile + 1 < tiles && w == kWaves - 1 && ln.live) {
-        const float2 *mine = &maps[w][0][lane];
-#pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            const float2 m = mine[e * 64];
-            put(hand.states + (int64_t)(tile / kGroupTiles + 1) * p.D + ln.c + e, 0.f, starts ? m.y : fmaf(m.x, h[e], m.y));
-        }
-    }
+    carry_in<VC, W>(x, hand, lane, w, tile, tiles, q.first_token < t0, q.first_token / TT, starts != 0, A, b, h);
     E *y = (E *)p.y + (int64_t)tw * p.D + ln.c;
-    seq = __builtin_amdgcn_readfirstlane(seq);
+    int seq = ends ? sequence_before(q, w * S, lane) : 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const bool fresh = starts >> s & 1;
@@ -380,34 +443,175 @@ __global__ void __launch_bounds__(kWaves * 64) scan_kernel(ScanParams p, int ncb
     }
 }
 
-template <typename E, typename G> __global__ void __launch_bounds__(256) scan_bwd_kernel(ScanParams p, int cblocks) {
-    const int n = blockIdx.x / cblocks, c = blockIdx.x % cblocks * 256 + threadIdx.x;
-    if (c >= p.D) return;
-    int t0, t1;
-    seq_range(p.cu_seqlens, n, p.T, p.T_tot, t0, t1);
-    const int64_t at = (int64_t)n * p.D + c;
-    const int groups = (p.D + kGroup - 1) / kGroup;
-    auto held = [&](const Held &h8, int64_t t) {
-        return (float)((const int8_t *)h8.codes)[t * p.D + c] *
-               (float)((const bf16 *)h8.scales)[t * groups + c / kGroup];
-    };
-    float carry = p.dht ? p.dht[at] : 0.f;
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-        const float a = decay(to_f(((const G *)p.g)[t * p.g_stride + c]));
-        const float dh = to_f(((const E *)p.dy)[t * p.D + c]) + carry;
-        carry = a * dh;
-        const float before = t == t0 ? (p.initial ? ((const float *)p.initial)[at] : 0.f)
-                             : p.y8.codes ? held(p.y8, t - 1) : to_f(((const E *)p.y)[(t - 1) * p.D + c]);
-        ((G *)p.dg)[t * p.D + c] = to_e<G>(carry * before);
-        float dx = dh;
-        if (p.beta) {
-            const float x = p.x8.codes ? held(p.x8, t) : to_f(((const E *)p.x)[t * p.x_stride + c]);
-            ((G *)p.dbeta)[t * p.D + c] = to_e<G>(x * dh);
-            dx *= to_f(((const G *)p.beta)[t * p.beta_stride + c]);
-        }
-        ((E *)p.dx)[t * p.D + c] = to_e<E>(dx);
+// VC values of a row as they are, or in 8 bits: as loaded, and as fp32.  The values
+// of a lane may lie in two groups.
+template <typename E, int VC, bool HELD> struct Saved {
+    typename Vector<E, VC>::T r;
+    __device__ __forceinline__ void clear() { r = Vector<E, VC>::zero(); }
+    __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int D, int c) {
+        r = Vector<E, VC>::load((const E *)v + row * stride + c);
     }
-    if (p.dinitial) p.dinitial[at] = carry;
+    __device__ __forceinline__ float get(int e, int) const { return Vector<E, VC>::get(r, e); }
+};
+typedef uint32_t u32u __attribute__((aligned(1)));
+template <typename E, int VC> struct Saved<E, VC, true> {
+    uint32_t codes;
+    bf16 s0, s1;
+    __device__ __forceinline__ void clear() {
+        codes = 0;
+        s0 = s1 = (bf16)0.f;
+    }
+    __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, int c) {
+        const uint8_t *src = (const uint8_t *)h.codes + row * D + c;
+        const bf16 *sc = (const bf16 *)h.scales + row * ((D + kGroup - 1) / kGroup);
+        codes = VC == 4 ? *(const u32u *)src : *src;
+        s0 = sc[c / kGroup];
+        s1 = VC == 1 ? s0 : sc[(c + VC - 1) / kGroup];
+    }
+    __device__ __forceinline__ float get(int e, int c) const {
+        return held_byte(codes, e) * (float)((c + e) / kGroup == c / kGroup ? s0 : s1);
+    }
+};
+
+template <typename E, typename G, bool BETA, bool HELD, int VC, int W, int S>
+__global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb, int tiles) {
+    constexpr int NT = W * 64, TT = W * S;
+    __shared__ Sequences<TT> q;
+    __shared__ Exchange<VC, W> x;
+    __shared__ int ticket;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int id = next_tile(p.ws, tiles, &ticket);
+    const Handed hand = handed_of<VC>(p.ws, tiles, ncb, id % ncb, lane);
+    const int place = id / ncb, tile = tiles - 1 - place, t0 = tile * TT;
+    const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
+    const int t_end = p.cu_seqlens ? cu_at(p.cu_seqlens, p.N, p.T_tot) : p.T_tot;
+    {
+        // the gradient of an empty sequence's initial state is that of its final state
+        ScanParams e = p;
+        e.initial = p.dht;
+        e.final_state = p.dinitial;
+        empty_sequences<VC, W>(e, tile, tiles, ln.c, ln.live);
+    }
+    if (t0 >= t_end) return;
+    const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the wave's tokens
+
+    typedef Vector<E, VC> RE;
+    typedef Vector<G, VC> RG;
+    typedef Saved<E, VC, HELD> SV;
+    float a[S][VC], d[S][VC];                          // decays; gradients of y, then of the state
+    {
+        typename RE::T dr[S];
+        typename RG::T gr[S];
+        const E *dp = (const E *)p.dy + (int64_t)tw * p.D;
+        const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            dr[s] = RE::zero();
+            gr[s] = RG::zero();
+            if (s < nv && ln.live) {
+                dr[s] = RE::load(dp + (int64_t)s * p.D + ln.c);
+                gr[s] = RG::load(gp + s * p.g_stride + ln.c);
+            }
+        }
+        find_sequences<TT, NT>(q, p, t0, t_end);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                a[s][e] = decay(RG::get(gr[s], e));
+                d[s][e] = RE::get(dr[s], e);
+            }
+    }
+    // what the gradients of the gates take, on its way while the tiles wait
+    SV yr[S], xr[S];
+    typename RG::T br[S];
+    {
+        const G *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            yr[s].clear();
+            if (BETA) {
+                xr[s].clear();
+                br[s] = RG::zero();
+            }
+            if (s < nv && ln.live) {
+                yr[s].load(p.y, p.y8, max(tw + s - 1, 0), p.D, p.D, ln.c);
+                if (BETA) {
+                    xr[s].load(p.x, p.x8, tw + s, p.x_stride, p.D, ln.c);
+                    br[s] = RG::load(bp + s * p.beta_stride + ln.c);
+                }
+            }
+        }
+    }
+    const bool is = lane < nv;
+    const int at = w * S + min(lane, S - 1);
+    const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
+    const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
+    const int seq = ends ? sequence_before(q, w * S, lane) : 0;   // of the wave's first token, unless one begins with it
+    float A[VC], c[VC], b[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e) {
+        A[e] = 1.f;
+        b[e] = 0.f;
+    }
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        if (ends >> s & 1) {
+            const uint32_t up_to = starts & ((2u << s) - 1);
+            const int n = up_to ? __builtin_amdgcn_readfirstlane(q.start[w * S + 31 - __builtin_clz(up_to)]) : seq;
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                if (p.dht && ln.live) d[s][e] += p.dht[(int64_t)n * p.D + ln.c + e];
+                b[e] = a[s][e] * d[s][e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VC; ++e) b[e] = a[s][e] * (d[s][e] + b[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < VC; ++e) A[e] *= a[s][e];
+    }
+    // whether a gradient comes into the tile, and from where on
+    const int count = min(TT, t_end - t0), last = sequence_before(q, count, lane);
+    const bool waits = q.start[count] < 0 && t0 + count < t_end;
+    const int end = p.cu_seqlens ? min(cu_at(p.cu_seqlens, last + 1, p.T_tot), t_end) : (last + 1) * p.T;
+    carry_in<VC, W>(x, hand, lane, W - 1 - w, place, tiles, waits, tiles - 1 - (max(end, t0 + count) - 1) / TT, ends != 0, A, b,
+                    c);
+    const int64_t out = (int64_t)tw * p.D + ln.c;
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        const bool first = starts >> s & 1;
+        int n = 0;
+        float h0[VC];
+        if (first) {
+            n = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+#pragma unroll
+            for (int e = 0; e < VC; ++e)
+                h0[e] = p.initial && ln.live ? ((const float *)p.initial)[(int64_t)n * p.D + ln.c + e] : 0.f;
+        }
+        typename RE::T ox = RE::zero();
+        typename RG::T og = RG::zero(), ob = RG::zero();
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            const float dh = ends >> s & 1 ? d[s][e] : d[s][e] + c[e];
+            c[e] = a[s][e] * dh;
+            RG::set(og, e, c[e] * (first ? h0[e] : yr[s].get(e, ln.c)));
+            if (BETA) {
+                RG::set(ob, e, xr[s].get(e, ln.c) * dh);
+                RE::set(ox, e, RG::get(br[s], e) * dh);
+            } else {
+                RE::set(ox, e, dh);
+            }
+        }
+        if (s < nv && ln.live) {
+            RE::store((E *)p.dx + out + (int64_t)s * p.D, ox);
+            RG::store((G *)p.dg + out + (int64_t)s * p.D, og);
+            if (BETA) RG::store((G *)p.dbeta + out + (int64_t)s * p.D, ob);
+        }
+        if (first && p.dinitial && ln.live)
+#pragma unroll
+            for (int e = 0; e < VC; ++e) p.dinitial[(int64_t)n * p.D + ln.c + e] = c[e];
+    }
 }
 
 // A few tokens per sequence, states in a pool: see StepSlots.
@@ -436,34 +640,42 @@ template <typename E, typename G> __global__ void __launch_bounds__(256) scan_st
     }
 }
 
-constexpr int kTokens = 16;                            // of a wave
-int tiles_of(int64_t T_tot) { return (int)((T_tot + kWaves * kTokens - 1) / (kWaves * kTokens)); }
+enum Pass { kForward, kBackward, kSteps };
+// Waves of a workgroup and tokens of a wave.
+struct Tile {
+    int W, S;
+};
+constexpr Tile kForwardTile{8, 16}, kBackwardTile{8, 8};
+int tiles_of(int64_t T_tot, Tile t) { return (int)std::max<int64_t>((T_tot + t.W * t.S - 1) / (t.W * t.S), 1); }
 // Four channels a lane; rows of fewer have one.
 int blocks_of(int D) { return D < 4 ? column_blocks<1>(D) : column_blocks<4>(D); }
 
-enum Pass { kForward, kBackward, kSteps };
-template <typename E, typename G, bool BETA, int VC> void launch_tiles(const ScanParams &p, hipStream_t st) {
-    const int tiles = std::max(tiles_of(p.T_tot), 1), ncb = column_blocks<VC>(p.D);
+template <typename E, typename G, bool BETA, bool HELD, int VC> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
+    const int tiles = tiles_of(p.T_tot, pass == kForward ? kForwardTile : kBackwardTile), ncb = column_blocks<VC>(p.D);
     if (tiles > 1) {
-        const int64_t n = (handed_words(tiles, p.D) + 1) / 2;
+        const int64_t n = handed_words(tiles, (int64_t)ncb * VC * 64) / 2;
         clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>((uint4 *)p.ws, n);
     }
-    scan_kernel<E, G, BETA, VC, kTokens><<<(unsigned)(tiles * ncb), kWaves * 64, 0, st>>>(p, ncb, tiles);
+    const unsigned grid = (unsigned)(tiles * ncb);
+    if (pass == kBackward) {
+        scan_bwd_kernel<E, G, BETA, HELD, VC, kBackwardTile.W, kBackwardTile.S><<<grid, kBackwardTile.W * 64, 0, st>>>(p, ncb, tiles);
+    } else if constexpr (!HELD) {
+        scan_kernel<E, G, BETA, VC, kForwardTile.W, kForwardTile.S><<<grid, kForwardTile.W * 64, 0, st>>>(p, ncb, tiles);
+    }
+}
+template <typename E, typename G, bool HELD> void launch_vc(const ScanParams &p, Pass pass, hipStream_t st) {
+    if (p.D < 4)
+        p.beta ? launch_tiles<E, G, true, HELD, 1>(p, pass, st) : launch_tiles<E, G, false, HELD, 1>(p, pass, st);
+    else
+        p.beta ? launch_tiles<E, G, true, HELD, 4>(p, pass, st) : launch_tiles<E, G, false, HELD, 4>(p, pass, st);
 }
 template <typename E, typename G> void launch_e(const ScanParams &p, Pass pass, hipStream_t st) {
-    if (pass == kForward) {
-        if (p.D < 4)
-            p.beta ? launch_tiles<E, G, true, 1>(p, st) : launch_tiles<E, G, false, 1>(p, st);
-        else
-            p.beta ? launch_tiles<E, G, true, 4>(p, st) : launch_tiles<E, G, false, 4>(p, st);
+    if (pass != kSteps) {
+        p.y8.codes ? launch_vc<E, G, true>(p, pass, st) : launch_vc<E, G, false>(p, pass, st);
         return;
     }
     const int cblocks = (p.D + 255) / 256;
-    const unsigned grid = (unsigned)((int64_t)p.N * cblocks);
-    if (pass == kBackward)
-        scan_bwd_kernel<E, G><<<grid, 256, 0, st>>>(p, cblocks);
-    else
-        scan_steps_kernel<E, G><<<grid, 256, 0, st>>>(p, cblocks);
+    scan_steps_kernel<E, G><<<(unsigned)((int64_t)p.N * cblocks), 256, 0, st>>>(p, cblocks);
 }
 hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, hipStream_t st, Profiler *prof) {
     if (p.N == 0) return hipSuccess;
@@ -482,12 +694,13 @@ hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, h
 
 }  // namespace
 
-size_t scan_workspace_bytes(int64_t T_tot, int D, int, int, bool) {
-    const int tiles = tiles_of(T_tot);
-    return tiles > 1 ? (size_t)(handed_words(tiles, D) + 1) / 2 * 16 : 0;
+size_t scan_workspace_bytes(int64_t T_tot, int D, int, int, bool backward) {
+    const int tiles = tiles_of(T_tot, backward ? kBackwardTile : kForwardTile);
+    return tiles > 1 ? (size_t)handed_words(tiles, (int64_t)blocks_of(D) * (D < 4 ? 1 : 4) * 64) * 8 : 0;
 }
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N) {
-    return std::max(N * ((D + 255) / 256), (int64_t)tiles_of(T_tot) * blocks_of((int)D));
+    const int64_t tiles = std::max(tiles_of(T_tot, kForwardTile), tiles_of(T_tot, kBackwardTile));
+    return std::max(N * ((D + 255) / 256), tiles * blocks_of((int)D));
 }
 
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof) {
