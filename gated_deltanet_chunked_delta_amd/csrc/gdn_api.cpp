@@ -506,8 +506,7 @@ gdn::ScanParams scan_params(const gdn_scan_shape &s, const void *x, const void *
 }
 int scan_gate_f32(const gdn_scan_shape &s) { return s.gate_dtype == GDN_F32; }
 int check_scan_ws(const gdn_scan_shape &s, bool backward, const void *workspace, size_t workspace_bytes) {
-    const size_t need =
-        gdn::scan_workspace_bytes((int64_t)s.B * s.T, s.D, s.dtype, scan_gate_f32(s), backward);
+    const size_t need = gdn::scan_workspace_bytes((int64_t)s.B * s.T, s.D, scan_gate_f32(s), backward);
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GDN_ERR_WORKSPACE;
     return GDN_OK;
 }
@@ -931,7 +930,7 @@ size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward) {
     if (gdn::elem_bytes(shape->dtype) == 0 || gdn::elem_bytes(shape->gate_dtype) == 0) return 0;
     const int64_t tokens = (int64_t)shape->B * shape->T;
     if (tokens > INT_MAX - 64) return 0;
-    return gdn::scan_workspace_bytes(tokens, shape->D, shape->dtype, scan_gate_f32(*shape), backward != 0);
+    return gdn::scan_workspace_bytes(tokens, shape->D, scan_gate_f32(*shape), backward != 0);
 }
 
 int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state,

@@ -139,7 +139,7 @@ struct ScanParams {
     int T, T_tot, D, N;
 };
 // gate_f32: g, beta and their gradients are fp32 (else the element type).
-size_t scan_workspace_bytes(int64_t T_tot, int D, int dtype, int gate_f32, bool backward);
+size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward);
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N);
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
 hipError_t launch_scan_bwd(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);

@@ -5,6 +5,7 @@
 //   dx = beta dh,  dbeta = x dh,  dg_t = e^(g_t) h_(t-1) dh_t,  dh0 = e^(g_1) dh_1
 // with h_(t-1) the forward's y_(t-1) as it was rounded, or the initial state.
 #include <algorithm>
+#include <type_traits>
 
 // Products and sums are fused where fmaf says so and nowhere else: two lanes that
 // share a channel (see lane_of) compute it at different places of their vectors and
@@ -37,28 +38,69 @@ __device__ __forceinline__ float decay(float g) {
     return g < -87.f ? 0.f : __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));   // NaN for a NaN
 }
 
-// One element as Raw has four and eight.
-template <typename E> struct RawOne {
+// VC = 1, 2 or 4 consecutive elements, as loaded, at any address.  S: past the caches.
+template <typename E, int VC> struct Vector : Raw<E, VC> {};
+template <typename E> struct Vector<E, 2> {
+    typedef typename Two<E>::T T;
+    typedef typename Two<E>::U U;
+    template <bool S = false> static __device__ __forceinline__ T load(const E *p) {
+        if constexpr (S)
+            return __builtin_nontemporal_load((const U *)p);
+        else
+            return *(const U *)p;
+    }
+    template <bool S = false> static __device__ __forceinline__ void store(E *p, T r) {
+        if constexpr (S)
+            __builtin_nontemporal_store(r, (U *)p);
+        else
+            *(U *)p = r;
+    }
+    static __device__ __forceinline__ T zero() { return T{}; }
+    static __device__ __forceinline__ float get(T r, int e) { return to_f(r[e]); }
+    static __device__ __forceinline__ void set(T &r, int e, float x) { r[e] = to_e<E>(x); }
+};
+template <typename E> struct Vector<E, 1> {
     typedef E T;
-    static __device__ __forceinline__ T load(const E *p) { return *p; }
-    static __device__ __forceinline__ void store(E *p, T r) { *p = r; }
+    template <bool S = false> static __device__ __forceinline__ T load(const E *p) { return *p; }
+    template <bool S = false> static __device__ __forceinline__ void store(E *p, T r) { *p = r; }
     static __device__ __forceinline__ T zero() { return to_e<E>(0.f); }
     static __device__ __forceinline__ float get(T r, int) { return to_f(r); }
     static __device__ __forceinline__ void set(T &r, int, float x) { r = to_e<E>(x); }
 };
-template <typename E, int VC> struct Vector : Raw<E, VC> {};
-template <typename E> struct Vector<E, 1> : RawOne<E> {};
 
-__device__ __forceinline__ float load_state(const void *s, int64_t at, int b16) {
-    return b16 ? (float)((const bf16 *)s)[at] : ((const float *)s)[at];
-}
-__device__ __forceinline__ void store_state(void *s, int64_t at, int b16, float h) {
-    if (b16)
-        ((bf16 *)s)[at] = (bf16)h;
-    else
-        ((float *)s)[at] = h;
+// A value that the compiler takes to be another one, so that what was computed from it
+// is computed again instead of being kept.
+template <typename T> __device__ __forceinline__ void forget(T &r) {
+    typedef std::conditional_t<sizeof(T) == 8, unsigned long long, std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>> U;
+    U v = __builtin_bit_cast(U, r);
+    asm("" : "+v"(v));
+    r = __builtin_bit_cast(T, v);
 }
 
+template <int VC> __device__ __forceinline__ void load_states(const void *s, int64_t at, int b16, float *h) {
+    if (b16) {
+        const typename Vector<bf16, VC>::T r = Vector<bf16, VC>::load((const bf16 *)s + at);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) h[e] = Vector<bf16, VC>::get(r, e);
+    } else {
+        const typename Vector<float, VC>::T r = Vector<float, VC>::load((const float *)s + at);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) h[e] = Vector<float, VC>::get(r, e);
+    }
+}
+template <int VC> __device__ __forceinline__ void store_states(void *s, int64_t at, int b16, const float *h) {
+    if (b16) {
+        typename Vector<bf16, VC>::T r;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) Vector<bf16, VC>::set(r, e, h[e]);
+        Vector<bf16, VC>::store((bf16 *)s + at, r);
+    } else {
+        typename Vector<float, VC>::T r;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) Vector<float, VC>::set(r, e, h[e]);
+        Vector<float, VC>::store((float *)s + at, r);
+    }
+}
 // ---------------------------------------------------------------------------
 // Tiles.  The tokens of all sequences lie on one axis, which is cut into tiles of
 // W * S tokens; a workgroup of W waves takes one tile of up to 64 * VC channels,
@@ -194,8 +236,11 @@ __device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, i
             if (slot < 0 || slot >= p.pool_size) continue;
             at = (int64_t)slot * p.D + c;
         }
+        float h[VC];
 #pragma unroll
-        for (int e = 0; e < VC; ++e) store_state(p.final_state, at + e, p.state_bf16, p.initial ? load_state(p.initial, at + e, p.state_bf16) : 0.f);
+        for (int e = 0; e < VC; ++e) h[e] = 0.f;
+        if (p.initial) load_states<VC>(p.initial, at, p.state_bf16, h);
+        store_states<VC>(p.final_state, at, p.state_bf16, h);
     }
 }
 
@@ -228,6 +273,7 @@ template <int VC, int W> struct Exchange {
 template <int VC, int W>
 __device__ __forceinline__ void fetch(Exchange<VC, W> &x, const Handed &hand, int lane, int rank, int lo, int hi, int from,
                                       int nt, int gfrom, int ng, int block) {
+#pragma unroll 1
     for (int k = lo + rank; k < hi; k += W) {
         const unsigned long long *src = k < nt        ? hand.tiles + (from + k) * hand.row
                                         : k < nt + ng ? hand.groups + (gfrom + k - nt) * hand.row
@@ -260,6 +306,7 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
         Ae[e] = 1.f;
         he[e] = 0.f;
     }
+#pragma unroll 1
     for (int k = 0; k < rank; ++k) {
         const bool anew = x.cut[k] != 0;
         own = own || anew;
@@ -291,6 +338,7 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
     if (waits) {
         fetch<VC, W>(x, hand, lane, rank, 0, ends_group ? nt : all, from, nt, gfrom, ng, block);
         lds_barrier();
+#pragma unroll 1
         for (int k = 0; k < nt; ++k)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
@@ -314,6 +362,7 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
         if (further)
 #pragma unroll
             for (int e = 0; e < VC; ++e) hin[e] = x.before[nt + ng][e][lane].y;
+#pragma unroll 1
         for (int k = 0; k < ng; ++k)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
@@ -332,8 +381,8 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
     }
 }
 
-template <typename E, typename G, bool BETA, int VC, int W, int S>
-__global__ void __launch_bounds__(W * 64) scan_kernel(ScanParams p, int ncb, int tiles) {
+template <typename E, typename G, bool BETA, bool STREAM, int VC, int W, int S>
+__global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, int tiles) {
     constexpr int NT = W * 64, TT = W * S;
     __shared__ Sequences<TT> q;
     __shared__ Exchange<VC, W> x;
@@ -350,24 +399,27 @@ __global__ void __launch_bounds__(W * 64) scan_kernel(ScanParams p, int ncb, int
 
     typedef Vector<E, VC> RE;
     typedef Vector<G, VC> RG;
-    float a[S][VC], u[S][VC];
-    {
-        typename RE::T xr[S];
-        typename RG::T gr[S], br[S];
-        const E *xp = (const E *)p.x + (int64_t)tw * p.x_stride;
-        const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
+    // bf16 gates stay as they were loaded and their decays are taken twice (2 or 3
+    // registers a token and two channels instead of 4); others become decays and inputs
+    constexpr bool RAW = sizeof(G) == 2;
+    typename RE::T xr[S];
+    typename RG::T gr[S], br[S];
+    float a[RAW ? 1 : S][VC], u[RAW ? 1 : S][VC];
+    const E *xp = (const E *)p.x + (int64_t)tw * p.x_stride;
+    const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            xr[s] = RE::zero();
-            gr[s] = RG::zero();                        // a = 1, u = 0: the state stays
-            if (BETA) br[s] = RG::zero();
-            if (s < nv && ln.live) {
-                xr[s] = RE::load(xp + s * p.x_stride + ln.c);
-                gr[s] = RG::load(gp + s * p.g_stride + ln.c);
-                if (BETA) br[s] = RG::load(bp + s * p.beta_stride + ln.c);
-            }
+    for (int s = 0; s < S; ++s) {
+        xr[s] = RE::zero();
+        gr[s] = RG::zero();                            // a = 1, u = 0: the state stays
+        if (BETA) br[s] = RG::zero();
+        if (s < nv && ln.live) {
+            xr[s] = RE::template load<STREAM>(xp + s * p.x_stride + ln.c);
+            gr[s] = RG::template load<STREAM>(gp + s * p.g_stride + ln.c);
+            if (BETA) br[s] = RG::template load<STREAM>(bp + s * p.beta_stride + ln.c);
         }
-        find_sequences<TT, NT>(q, p, t0, t_end);
+    }
+    find_sequences<TT, NT>(q, p, t0, t_end);
+    if constexpr (!RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -376,58 +428,86 @@ __global__ void __launch_bounds__(W * 64) scan_kernel(ScanParams p, int ncb, int
                 u[s][e] = RE::get(xr[s], e);
                 if (BETA) u[s][e] *= RG::get(br[s], e);
             }
-    }
+    auto token = [&](int s, int e, float &av, float &uv) {
+        if constexpr (RAW) {
+            av = decay(RG::get(gr[s], e));
+            uv = RE::get(xr[s], e);
+            if (BETA) uv *= RG::get(br[s], e);
+        } else {
+            av = a[s][e];
+            uv = u[s][e];
+        }
+    };
     // sequences that begin at, or end with, the wave's tokens
     const bool is = lane < nv;
     const int at = w * S + min(lane, S - 1);
     const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
     const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
-    float A[VC], h[VC], b[VC];
+    auto initial = [&](int n, float *h) {
+        int64_t from = (int64_t)n * p.D + ln.c;
+        bool has = p.initial != nullptr && ln.live;
+        if (p.indices) {
+            const int slot = p.indices[n];
+            has = has && slot >= 0 && slot < p.pool_size;
+            from = (int64_t)slot * p.D + ln.c;
+        }
+#pragma unroll
+        for (int e = 0; e < VC; ++e) h[e] = 0.f;
+        if (has) load_states<VC>(p.initial, from, p.state_bf16, h);
+    };
+    float A[VC], h[VC], b[VC], h0[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
         A[e] = 1.f;
-        b[e] = 0.f;
+        b[e] = h0[e] = 0.f;
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        if (starts >> s & 1) {
-            // The state that the sequence starts from takes the place of the one that
-            // came in.  It is read once, before the tile's map is handed on: its
-            // buffer may be the final state's.
-            const int n = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
-            int64_t from = (int64_t)n * p.D + ln.c;
-            bool has = p.initial != nullptr && ln.live;
-            if (p.indices) {
-                const int slot = p.indices[n];
-                has = has && slot >= 0 && slot < p.pool_size;
-                from = (int64_t)slot * p.D + ln.c;
-            }
+        if (starts >> s & 1) {                         // what came in is replaced
+            initial(__builtin_amdgcn_readfirstlane(q.start[w * S + s]), h0);
 #pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                const float h0 = has ? load_state(p.initial, from + e, p.state_bf16) : 0.f;
-                b[e] = u[s][e] = fmaf(a[s][e], h0, u[s][e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VC; ++e) b[e] = fmaf(a[s][e], b[e], u[s][e]);
+            for (int e = 0; e < VC; ++e) b[e] = h0[e];
         }
 #pragma unroll
-        for (int e = 0; e < VC; ++e) A[e] *= a[s][e];
+        for (int e = 0; e < VC; ++e) {
+            float av, uv;
+            token(s, e, av, uv);
+            b[e] = fmaf(av, b[e], uv);
+            A[e] *= av;
+        }
     }
     carry_in<VC, W>(x, hand, lane, w, tile, tiles, q.first_token < t0, q.first_token / TT, starts != 0, A, b, h);
+    if constexpr (RAW)
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            forget(gr[s]);
+            if constexpr (sizeof(E) == 2) forget(xr[s]);
+            if (BETA) forget(br[s]);
+        }
     E *y = (E *)p.y + (int64_t)tw * p.D + ln.c;
     int seq = ends ? sequence_before(q, w * S, lane) : 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        const bool fresh = starts >> s & 1;
-        if (fresh) seq = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+        if (starts >> s & 1) {
+            // The last sequence that begins here may end with another wave, which may have
+            // stored its final state where its initial state was: that one is h0 still.
+            // The others end here.
+            seq = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+            if (starts >> s != 1)
+                initial(seq, h);
+            else
+#pragma unroll
+                for (int e = 0; e < VC; ++e) h[e] = h0[e];
+        }
         typename RE::T o = RE::zero();
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            h[e] = fresh ? u[s][e] : fmaf(a[s][e], h[e], u[s][e]);
+            float av, uv;
+            token(s, e, av, uv);
+            h[e] = fmaf(av, h[e], uv);
             RE::set(o, e, h[e]);
         }
-        if (s < nv && ln.live) RE::store(y + (int64_t)s * p.D, o);
+        if (s < nv && ln.live) RE::template store<STREAM>(y + (int64_t)s * p.D, o);
         if ((ends >> s & 1) && p.final_state && ln.live) {
             int64_t to = (int64_t)seq * p.D + ln.c;
             bool kept = true;
@@ -436,45 +516,41 @@ __global__ void __launch_bounds__(W * 64) scan_kernel(ScanParams p, int ncb, int
                 kept = slot >= 0 && slot < p.pool_size;
                 to = (int64_t)slot * p.D + ln.c;
             }
-            if (kept)
-#pragma unroll
-                for (int e = 0; e < VC; ++e) store_state(p.final_state, to + e, p.state_bf16, h[e]);
+            if (kept) store_states<VC>(p.final_state, to, p.state_bf16, h);
         }
     }
 }
 
-// VC values of a row as they are, or in 8 bits: as loaded, and as fp32.  The values
-// of a lane may lie in two groups.
-template <typename E, int VC, bool HELD> struct Saved {
+// VC values of a row as they are, or in 8 bits: as loaded, and as fp32.  Of held ones
+// those of a lane lie in two groups where vectors overlap (two, see lane_of).
+template <typename E, int VC, bool HELD, bool STREAM> struct Saved {
     typename Vector<E, VC>::T r;
     __device__ __forceinline__ void clear() { r = Vector<E, VC>::zero(); }
-    __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int D, int c) {
-        r = Vector<E, VC>::load((const E *)v + row * stride + c);
+    __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int, int c, bool) {
+        r = Vector<E, VC>::template load<STREAM>((const E *)v + row * stride + c);
     }
-    __device__ __forceinline__ float get(int e, int) const { return Vector<E, VC>::get(r, e); }
+    __device__ __forceinline__ float get(int e, int, bool) const { return Vector<E, VC>::get(r, e); }
 };
 typedef uint32_t u32u __attribute__((aligned(1)));
-template <typename E, int VC> struct Saved<E, VC, true> {
-    uint32_t codes;
-    bf16 s0, s1;
-    __device__ __forceinline__ void clear() {
-        codes = 0;
-        s0 = s1 = (bf16)0.f;
-    }
-    __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, int c) {
+typedef uint16_t u16u __attribute__((aligned(1)));
+template <typename E, int VC, bool STREAM> struct Saved<E, VC, true, STREAM> {
+    uint32_t codes, scales;                            // scales: of the first value's group low, of the last one's high
+    __device__ __forceinline__ void clear() { codes = scales = 0; }
+    __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, int c, bool two) {
         const uint8_t *src = (const uint8_t *)h.codes + row * D + c;
-        const bf16 *sc = (const bf16 *)h.scales + row * ((D + kGroup - 1) / kGroup);
-        codes = VC == 4 ? *(const u32u *)src : *src;
-        s0 = sc[c / kGroup];
-        s1 = VC == 1 ? s0 : sc[(c + VC - 1) / kGroup];
+        const uint16_t *sc = (const uint16_t *)h.scales + row * ((D + kGroup - 1) / kGroup);
+        codes = VC == 4 ? *(const u32u *)src : VC == 2 ? *(const u16u *)src : *src;
+        scales = sc[c / kGroup];
+        if (two) scales |= (uint32_t)sc[(c + VC - 1) / kGroup] << 16;
     }
-    __device__ __forceinline__ float get(int e, int c) const {
-        return held_byte(codes, e) * (float)((c + e) / kGroup == c / kGroup ? s0 : s1);
+    __device__ __forceinline__ float get(int e, int c, bool two) const {
+        const uint32_t s = two && (c + e) / kGroup != c / kGroup ? scales & 0xffff0000u : scales << 16;
+        return held_byte(codes, e) * __uint_as_float(s);
     }
 };
 
-template <typename E, typename G, bool BETA, bool HELD, int VC, int W, int S>
-__global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb, int tiles) {
+template <typename E, typename G, bool BETA, bool HELD, bool STREAM, int VC, int W, int S>
+__global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int ncb, int tiles) {
     constexpr int NT = W * 64, TT = W * S;
     __shared__ Sequences<TT> q;
     __shared__ Exchange<VC, W> x;
@@ -494,52 +570,52 @@ __global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb,
     }
     if (t0 >= t_end) return;
     const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the wave's tokens
+    const bool two = p.D % VC != 0;
 
     typedef Vector<E, VC> RE;
     typedef Vector<G, VC> RG;
-    typedef Saved<E, VC, HELD> SV;
-    float a[S][VC], d[S][VC];                          // decays; gradients of y, then of the state
-    {
-        typename RE::T dr[S];
-        typename RG::T gr[S];
-        const E *dp = (const E *)p.dy + (int64_t)tw * p.D;
-        const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride;
+    typedef Saved<E, VC, HELD, STREAM> SV;
+    constexpr bool RAW = sizeof(G) == 2;               // see scan_kernel
+    typename RE::T dr[S];
+    typename RG::T gr[S], br[S];
+    float a[RAW ? 1 : S][VC];
+    const E *dp = (const E *)p.dy + (int64_t)tw * p.D;
+    const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            dr[s] = RE::zero();
-            gr[s] = RG::zero();
-            if (s < nv && ln.live) {
-                dr[s] = RE::load(dp + (int64_t)s * p.D + ln.c);
-                gr[s] = RG::load(gp + s * p.g_stride + ln.c);
-            }
+    for (int s = 0; s < S; ++s) {
+        dr[s] = RE::zero();
+        gr[s] = RG::zero();
+        if (s < nv && ln.live) {
+            dr[s] = RE::template load<STREAM>(dp + (int64_t)s * p.D + ln.c);
+            gr[s] = RG::template load<STREAM>(gp + s * p.g_stride + ln.c);
         }
-        find_sequences<TT, NT>(q, p, t0, t_end);
+    }
+    find_sequences<TT, NT>(q, p, t0, t_end);
+    if constexpr (!RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                a[s][e] = decay(RG::get(gr[s], e));
-                d[s][e] = RE::get(dr[s], e);
-            }
-    }
+            for (int e = 0; e < VC; ++e) a[s][e] = decay(RG::get(gr[s], e));
+    auto decay_of = [&](int s, int e) {
+        if constexpr (RAW)
+            return decay(RG::get(gr[s], e));
+        else
+            return a[s][e];
+    };
     // what the gradients of the gates take, on its way while the tiles wait
     SV yr[S], xr[S];
-    typename RG::T br[S];
-    {
-        const G *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            yr[s].clear();
+    for (int s = 0; s < S; ++s) {
+        yr[s].clear();
+        if (BETA) {
+            xr[s].clear();
+            br[s] = RG::zero();
+        }
+        if (s < nv && ln.live) {
+            yr[s].load(p.y, p.y8, max(tw + s - 1, 0), p.D, p.D, ln.c, two);
             if (BETA) {
-                xr[s].clear();
-                br[s] = RG::zero();
-            }
-            if (s < nv && ln.live) {
-                yr[s].load(p.y, p.y8, max(tw + s - 1, 0), p.D, p.D, ln.c);
-                if (BETA) {
-                    xr[s].load(p.x, p.x8, tw + s, p.x_stride, p.D, ln.c);
-                    br[s] = RG::load(bp + s * p.beta_stride + ln.c);
-                }
+                xr[s].load(p.x, p.x8, tw + s, p.x_stride, p.D, ln.c, two);
+                br[s] = RG::template load<STREAM>(bp + s * p.beta_stride + ln.c);
             }
         }
     }
@@ -548,6 +624,14 @@ __global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb,
     const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
     const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
     const int seq = ends ? sequence_before(q, w * S, lane) : 0;   // of the wave's first token, unless one begins with it
+    // the gradient of the final state of the sequence that ends with token s
+    auto final_gradient = [&](int s, float *c) {
+        const uint32_t up_to = starts & ((2u << s) - 1);
+        const int n = up_to ? __builtin_amdgcn_readfirstlane(q.start[w * S + 31 - __builtin_clz(up_to)]) : seq;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) c[e] = 0.f;
+        if (p.dht && ln.live) load_states<VC>(p.dht, (int64_t)n * p.D + ln.c, 0, c);
+    };
     float A[VC], c[VC], b[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
@@ -556,27 +640,25 @@ __global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb,
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
-        if (ends >> s & 1) {
-            const uint32_t up_to = starts & ((2u << s) - 1);
-            const int n = up_to ? __builtin_amdgcn_readfirstlane(q.start[w * S + 31 - __builtin_clz(up_to)]) : seq;
+        if (ends >> s & 1) final_gradient(s, b);       // in the place of what came in
 #pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                if (p.dht && ln.live) d[s][e] += p.dht[(int64_t)n * p.D + ln.c + e];
-                b[e] = a[s][e] * d[s][e];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VC; ++e) b[e] = a[s][e] * (d[s][e] + b[e]);
+        for (int e = 0; e < VC; ++e) {
+            const float av = decay_of(s, e);
+            b[e] = av * (RE::get(dr[s], e) + b[e]);
+            A[e] *= av;
         }
-#pragma unroll
-        for (int e = 0; e < VC; ++e) A[e] *= a[s][e];
     }
     // whether a gradient comes into the tile, and from where on
     const int count = min(TT, t_end - t0), last = sequence_before(q, count, lane);
     const bool waits = q.start[count] < 0 && t0 + count < t_end;
     const int end = p.cu_seqlens ? min(cu_at(p.cu_seqlens, last + 1, p.T_tot), t_end) : (last + 1) * p.T;
-    carry_in<VC, W>(x, hand, lane, W - 1 - w, place, tiles, waits, tiles - 1 - (max(end, t0 + count) - 1) / TT, ends != 0, A, b,
-                    c);
+    carry_in<VC, W>(x, hand, lane, W - 1 - w, place, tiles, waits, tiles - 1 - (max(end, t0 + count) - 1) / TT, ends != 0, A, b, c);
+    if constexpr (RAW)
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            forget(gr[s]);
+            forget(dr[s]);
+        }
     const int64_t out = (int64_t)tw * p.D + ln.c;
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
@@ -586,96 +668,153 @@ __global__ void __launch_bounds__(W * 64) scan_bwd_kernel(ScanParams p, int ncb,
         if (first) {
             n = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
 #pragma unroll
-            for (int e = 0; e < VC; ++e)
-                h0[e] = p.initial && ln.live ? ((const float *)p.initial)[(int64_t)n * p.D + ln.c + e] : 0.f;
+            for (int e = 0; e < VC; ++e) h0[e] = 0.f;
+            if (p.initial && ln.live) load_states<VC>(p.initial, (int64_t)n * p.D + ln.c, 0, h0);
         }
+        if (ends >> s & 1) final_gradient(s, c);
         typename RE::T ox = RE::zero();
         typename RG::T og = RG::zero(), ob = RG::zero();
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            const float dh = ends >> s & 1 ? d[s][e] : d[s][e] + c[e];
-            c[e] = a[s][e] * dh;
-            RG::set(og, e, c[e] * (first ? h0[e] : yr[s].get(e, ln.c)));
+            const float dh = RE::get(dr[s], e) + c[e];
+            c[e] = decay_of(s, e) * dh;
+            RG::set(og, e, c[e] * (first ? h0[e] : yr[s].get(e, ln.c, two)));
             if (BETA) {
-                RG::set(ob, e, xr[s].get(e, ln.c) * dh);
+                RG::set(ob, e, xr[s].get(e, ln.c, two) * dh);
                 RE::set(ox, e, RG::get(br[s], e) * dh);
             } else {
                 RE::set(ox, e, dh);
             }
         }
         if (s < nv && ln.live) {
-            RE::store((E *)p.dx + out + (int64_t)s * p.D, ox);
-            RG::store((G *)p.dg + out + (int64_t)s * p.D, og);
-            if (BETA) RG::store((G *)p.dbeta + out + (int64_t)s * p.D, ob);
+            RE::template store<STREAM>((E *)p.dx + out + (int64_t)s * p.D, ox);
+            RG::template store<STREAM>((G *)p.dg + out + (int64_t)s * p.D, og);
+            if (BETA) RG::template store<STREAM>((G *)p.dbeta + out + (int64_t)s * p.D, ob);
         }
-        if (first && p.dinitial && ln.live)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) p.dinitial[(int64_t)n * p.D + ln.c + e] = c[e];
+        if (first && p.dinitial && ln.live) store_states<VC>(p.dinitial, (int64_t)n * p.D + ln.c, 0, c);
     }
 }
 
-// A few tokens per sequence, states in a pool: see StepSlots.
-template <typename E, typename G> __global__ void __launch_bounds__(256) scan_steps_kernel(ScanParams p, int cblocks) {
-    const int n = blockIdx.x / cblocks, c = blockIdx.x % cblocks * 256 + threadIdx.x;
-    if (c >= p.D) return;
+// A few tokens per sequence, states in a pool: see StepSlots.  A wave takes the
+// channels of a column block of one sequence; kAhead tokens are loaded before the
+// first of them is used, as the wave's own stores are in the way of later loads.
+constexpr int kAhead = 4;
+template <typename E, typename G, bool BETA, int VC> __global__ void __launch_bounds__(64) scan_steps_kernel(ScanParams p, int ncb) {
+    typedef Vector<E, VC> RE;
+    typedef Vector<G, VC> RG;
+    const int n = blockIdx.x / ncb;
+    const Lane ln = lane_of<VC>(p.D, ncb, blockIdx.x % ncb, threadIdx.x);
+    if (!ln.live) return;
     int t0, t1;
     seq_range(p.cu_seqlens, n, p.T, p.T_tot, t0, t1);
     const int32_t *idx = p.slots.indices + (int64_t)n * p.slots.cols;
     const int a = p.slots.accepted ? min(max(p.slots.accepted[n], 1), p.slots.cols) : 1;
     const int first = idx[a - 1];
-    if (first < 0 || first >= p.slots.pool_size) {
-        for (int64_t t = t0; t < t1; ++t) ((E *)p.y)[t * p.D + c] = to_e<E>(0.f);
-        return;
+    const bool row = first >= 0 && first < p.slots.pool_size;
+    float h[VC];
+    if (row) load_states<VC>(p.slots.data, (int64_t)first * p.D + ln.c, p.state_bf16, h);
+    for (int64_t t = t0; t < t1; t += kAhead) {
+        typename RE::T xr[kAhead];
+        typename RG::T gr[kAhead], br[kAhead];
+        int slot[kAhead];
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+            if (t + s >= t1) break;
+            const int j = (int)(t - t0) + s, col = min(j, p.slots.cols - 1);
+            slot[s] = col == p.slots.cols - 1 && t + s != t1 - 1 ? -1 : idx[col];   // the last column: the last token's
+            if (!row) continue;
+            xr[s] = RE::load((const E *)p.x + (t + s) * p.x_stride + ln.c);
+            gr[s] = RG::load((const G *)p.g + (t + s) * p.g_stride + ln.c);
+            if (BETA) br[s] = RG::load((const G *)p.beta + (t + s) * p.beta_stride + ln.c);
+        }
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+            if (t + s >= t1) break;
+            typename RE::T o = RE::zero();
+            if (row) {
+#pragma unroll
+                for (int e = 0; e < VC; ++e) {
+                    float u = RE::get(xr[s], e);
+                    if (BETA) u *= RG::get(br[s], e);
+                    h[e] = fmaf(decay(RG::get(gr[s], e)), h[e], u);
+                    RE::set(o, e, h[e]);
+                }
+                if (slot[s] >= 0 && slot[s] < p.slots.pool_size)
+                    store_states<VC>(p.slots.data, (int64_t)slot[s] * p.D + ln.c, p.state_bf16, h);
+            }
+            RE::store((E *)p.y + (t + s) * p.D + ln.c, o);
+        }
     }
-    float h = load_state(p.slots.data, (int64_t)first * p.D + c, p.state_bf16);
-    for (int64_t t = t0; t < t1; ++t) {
-        float u = to_f(((const E *)p.x)[t * p.x_stride + c]);
-        if (p.beta) u *= to_f(((const G *)p.beta)[t * p.beta_stride + c]);
-        h = fmaf(decay(to_f(((const G *)p.g)[t * p.g_stride + c])), h, u);
-        ((E *)p.y)[t * p.D + c] = to_e<E>(h);
-        const int j = (int)(t - t0), col = min(j, p.slots.cols - 1);
-        if (col == p.slots.cols - 1 && t != t1 - 1) continue;
-        const int slot = idx[col];
-        if (slot >= 0 && slot < p.slots.pool_size) store_state(p.slots.data, (int64_t)slot * p.D + c, p.state_bf16, h);
-    }
+}
+
+constexpr int kStepsVec = 4;
+int steps_blocks(int D) { return D < kStepsVec ? column_blocks<1>(D) : column_blocks<kStepsVec>(D); }
+template <typename E, typename G, bool BETA> void launch_steps_vc(const ScanParams &p, hipStream_t st) {
+    const int ncb = steps_blocks(p.D);
+    const unsigned grid = (unsigned)((int64_t)p.N * ncb);
+    if (p.D < kStepsVec)
+        scan_steps_kernel<E, G, BETA, 1><<<grid, 64, 0, st>>>(p, ncb);
+    else
+        scan_steps_kernel<E, G, BETA, kStepsVec><<<grid, 64, 0, st>>>(p, ncb);
 }
 
 enum Pass { kForward, kBackward, kSteps };
-// Waves of a workgroup and tokens of a wave.
+// Channels of a lane, waves of a workgroup and tokens of a wave, for at least two
+// workgroups a CU (128 registers a lane) and few tiles to hand states through.
 struct Tile {
-    int W, S;
+    int VC, W, S;
 };
-constexpr Tile kForwardTile{8, 16}, kBackwardTile{8, 8};
-int tiles_of(int64_t T_tot, Tile t) { return (int)std::max<int64_t>((T_tot + t.W * t.S - 1) / (t.W * t.S), 1); }
-// Four channels a lane; rows of fewer have one.
-int blocks_of(int D) { return D < 4 ? column_blocks<1>(D) : column_blocks<4>(D); }
+constexpr Tile tile_of(bool gate_f32, bool backward, bool beta, bool held) {
+    if (backward) return gate_f32 ? Tile{4, 8, 4} : beta && !held ? Tile{2, 8, 16} : Tile{4, 8, 8};
+    return gate_f32 ? Tile{4, 8, 8} : Tile{2, 8, 16};
+}
+// Rows of fewer channels than a lane's have one a lane.
+constexpr Tile narrow(Tile t) { return {1, t.W, t.S}; }
+int tiles_of(int64_t T_tot, const Tile &t) { return (int)std::max<int64_t>((T_tot + t.W * t.S - 1) / (t.W * t.S), 1); }
+int blocks_of(int D, const Tile &t) { return t.VC == 1 ? column_blocks<1>(D) : t.VC == 2 ? column_blocks<2>(D) : column_blocks<4>(D); }
 
-template <typename E, typename G, bool BETA, bool HELD, int VC> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
-    const int tiles = tiles_of(p.T_tot, pass == kForward ? kForwardTile : kBackwardTile), ncb = column_blocks<VC>(p.D);
+// Passes over more than the 256 MiB of the last cache are streamed past it.
+template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
+    const int gates = p.beta ? 2 : 1, kept = p.y8.codes ? gates : gates * (int)sizeof(E);
+    const int token = pass == kForward ? 2 * sizeof(E) + gates * sizeof(G) : 2 * sizeof(E) + 2 * gates * sizeof(G) + kept;
+    return (int64_t)p.T_tot * p.D * token > 256 << 20;
+}
+template <typename E, typename G, bool BETA, bool HELD, bool NARROW> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
+    constexpr bool f32 = sizeof(G) == 4;
+    constexpr Tile f = NARROW ? narrow(tile_of(f32, false, BETA, HELD)) : tile_of(f32, false, BETA, HELD);
+    constexpr Tile b = NARROW ? narrow(tile_of(f32, true, BETA, HELD)) : tile_of(f32, true, BETA, HELD);
+    const Tile t = pass == kForward ? f : b;
+    const int tiles = tiles_of(p.T_tot, t), ncb = blocks_of(p.D, t);
     if (tiles > 1) {
-        const int64_t n = handed_words(tiles, (int64_t)ncb * VC * 64) / 2;
+        const int64_t n = handed_words(tiles, (int64_t)ncb * t.VC * 64) / 2;
         clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>((uint4 *)p.ws, n);
     }
     const unsigned grid = (unsigned)(tiles * ncb);
+    const bool stream = !NARROW && streams<E, G>(p, pass);
     if (pass == kBackward) {
-        scan_bwd_kernel<E, G, BETA, HELD, VC, kBackwardTile.W, kBackwardTile.S><<<grid, kBackwardTile.W * 64, 0, st>>>(p, ncb, tiles);
+        if (stream)
+            scan_bwd_kernel<E, G, BETA, HELD, !NARROW, b.VC, b.W, b.S><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
+        else
+            scan_bwd_kernel<E, G, BETA, HELD, false, b.VC, b.W, b.S><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
     } else if constexpr (!HELD) {
-        scan_kernel<E, G, BETA, VC, kForwardTile.W, kForwardTile.S><<<grid, kForwardTile.W * 64, 0, st>>>(p, ncb, tiles);
+        if (stream)
+            scan_kernel<E, G, BETA, !NARROW, f.VC, f.W, f.S><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
+        else
+            scan_kernel<E, G, BETA, false, f.VC, f.W, f.S><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
     }
 }
 template <typename E, typename G, bool HELD> void launch_vc(const ScanParams &p, Pass pass, hipStream_t st) {
-    if (p.D < 4)
-        p.beta ? launch_tiles<E, G, true, HELD, 1>(p, pass, st) : launch_tiles<E, G, false, HELD, 1>(p, pass, st);
+    if (p.D < tile_of(sizeof(G) == 4, pass == kBackward, p.beta != nullptr, HELD).VC)
+        p.beta ? launch_tiles<E, G, true, HELD, true>(p, pass, st) : launch_tiles<E, G, false, HELD, true>(p, pass, st);
     else
-        p.beta ? launch_tiles<E, G, true, HELD, 4>(p, pass, st) : launch_tiles<E, G, false, HELD, 4>(p, pass, st);
+        p.beta ? launch_tiles<E, G, true, HELD, false>(p, pass, st) : launch_tiles<E, G, false, HELD, false>(p, pass, st);
 }
 template <typename E, typename G> void launch_e(const ScanParams &p, Pass pass, hipStream_t st) {
     if (pass != kSteps) {
         p.y8.codes ? launch_vc<E, G, true>(p, pass, st) : launch_vc<E, G, false>(p, pass, st);
         return;
     }
-    const int cblocks = (p.D + 255) / 256;
-    scan_steps_kernel<E, G><<<(unsigned)((int64_t)p.N * cblocks), 256, 0, st>>>(p, cblocks);
+    p.beta ? launch_steps_vc<E, G, true>(p, st) : launch_steps_vc<E, G, false>(p, st);
 }
 hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, hipStream_t st, Profiler *prof) {
     if (p.N == 0) return hipSuccess;
@@ -694,13 +833,26 @@ hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, h
 
 }  // namespace
 
-size_t scan_workspace_bytes(int64_t T_tot, int D, int, int, bool backward) {
-    const int tiles = tiles_of(T_tot, backward ? kBackwardTile : kForwardTile);
-    return tiles > 1 ? (size_t)handed_words(tiles, (int64_t)blocks_of(D) * (D < 4 ? 1 : 4) * 64) * 8 : 0;
+// Over the tiles that calls of these sizes and types take: f(tile).
+template <typename F> void each_tile(int64_t D, int gate_f32, bool backward, F f) {
+    for (int i = 0; i < 4; ++i) {
+        const Tile t = tile_of(gate_f32 != 0, backward, i & 1, i & 2);
+        f(D < t.VC ? narrow(t) : t);
+    }
+}
+size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward) {
+    size_t most = 0;
+    each_tile(D, gate_f32, backward, [&](const Tile &t) {
+        const int tiles = tiles_of(T_tot, t);
+        if (tiles > 1) most = std::max(most, (size_t)handed_words(tiles, (int64_t)blocks_of(D, t) * t.VC * 64) * 8);
+    });
+    return most;
 }
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N) {
-    const int64_t tiles = std::max(tiles_of(T_tot, kForwardTile), tiles_of(T_tot, kBackwardTile));
-    return std::max(N * ((D + 255) / 256), tiles * blocks_of((int)D));
+    int64_t most = N * steps_blocks((int)D);
+    for (int i = 0; i < 4; ++i)
+        each_tile(D, i & 1, i & 2, [&](const Tile &t) { most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t)); });
+    return most;
 }
 
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof) {
