@@ -15,12 +15,9 @@ namespace {
 
 using namespace dev;
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
-
 // A lane's vectors are the row's eights in order, so that four neighbours make a
 // group of the format; the last one of a row may be short.
-template <typename E, int L, int NV>
+template <typename E, int L, int NV, bool STREAM>
 __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, Held x8, Held z8) {
     typedef Raw8<E> R;
     typedef typename R::T V;
@@ -32,12 +29,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
     E *__restrict__ y = (E *)p.y;
     const int D = p.D, groups = (D + kGroup - 1) / kGroup;
     const float inv = 1.f / (float)D;
+    const bool tails = D % 8 != 0;
     float w[NV][8];
     int cnt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         cnt[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], true, p.w_f32, w[i]);
+        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], tails, p.w_f32, w[i]);
     }
     V xa[NV], za[NV];
     auto load = [&](int64_t row) {
@@ -47,8 +45,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
                                                (int64_t)((uint32_t)row % (uint32_t)p.heads) * D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xa[i] = load_n<E>(x + at + (i * L + l) * 8, cnt[i], true);
-            za[i] = load_n<E>(z + zat + (i * L + l) * 8, cnt[i], true);
+            xa[i] = load_n<E, 8, STREAM>(x + at + (i * L + l) * 8, cnt[i], tails);
+            za[i] = load_n<E, 8, STREAM>(z + zat + (i * L + l) * 8, cnt[i], tails);
         }
     };
     auto keep = [&](const float *v, const Held &to, int64_t row, int i) {
@@ -63,10 +61,7 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
         const int col = (i * L + l) * 8;
         const uint32_t a = pack4(c), b = pack4(c + 4);
         uint8_t *dst = (uint8_t *)to.codes + row * D + col;
-        if (cnt[i] == 8)
-            *(u32x2u *)dst = u32x2u{a, b};
-        else
-            for (int e = 0; e < cnt[i]; ++e) dst[e] = (uint8_t)((e < 4 ? a : b) >> (8 * (e % 4)));
+        if (cnt[i] == 8 || tails) store_codes<STREAM>(dst, a, b, cnt[i]);
         if (l % 4 == 0 && cnt[i] > 0) ((bf16 *)to.scales)[row * groups + col / kGroup] = (bf16)s;
     };
     int64_t row = (int64_t)blockIdx.x * GPB + threadIdx.x / L;
@@ -88,14 +83,14 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
             V o;
 #pragma unroll
             for (int e = 0; e < 8; ++e) R::set(o, e, h[i][e] * r * w[i][e] * (g[i][e] * sigmoid_f(g[i][e])));
-            store_n<E>(y + row * D + (i * L + l) * 8, o, cnt[i], true);
+            store_n<E, 8, STREAM>(y + row * D + (i * L + l) * 8, o, cnt[i], tails);
             keep(h[i], x8, row, i);
             keep(g[i], z8, row, i);
         }
     }
 }
 
-template <typename E, int L, int NV>
+template <typename E, int L, int NV, bool STREAM>
 __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {
     typedef Raw8<E> R;
     typedef typename R::T V;
@@ -109,12 +104,13 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
     E *__restrict__ dx = (E *)p.dx, *__restrict__ dz = (E *)p.dz;
     const int D = p.D, groups = (D + kGroup - 1) / kGroup;
     const float inv = 1.f / (float)D;
+    const bool tails = D % 8 != 0;
     float w[NV][8], dw[NV][8];
     int cnt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         cnt[i] = min(max(D - (i * L + l) * 8, 0), 8);
-        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], true, p.w_f32, w[i]);
+        load_w<E>(p.weight, (i * L + l) * 8, cnt[i], tails, p.w_f32, w[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
     }
@@ -124,10 +120,7 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
         codes = u32x2{0, 0};
         scale = 0.f;
         if (cnt[i] > 0) scale = (float)((const bf16 *)h.scales)[row * groups + col / kGroup];
-        if (cnt[i] == 8)
-            codes = *(const u32x2u *)src;
-        else
-            for (int e = 0; e < cnt[i]; ++e) codes[e / 4] |= (uint32_t)src[e] << (8 * (e % 4));
+        if (cnt[i] == 8 || tails) codes = load_codes<STREAM>(src, cnt[i]);
     };
     V da[NV];
     u32x2 xc[NV], zc[NV];
@@ -135,7 +128,7 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
     auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            da[i] = load_n<E>(dy + row * D + (i * L + l) * 8, cnt[i], true);
+            da[i] = load_n<E, 8, STREAM>(dy + row * D + (i * L + l) * 8, cnt[i], tails);
             fetch(x8, row, i, xc[i], xs[i]);
             fetch(z8, row, i, zc[i], zs[i]);
         }
@@ -169,8 +162,8 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
                 R::set(oz, e, u[i][e] * nv * w[i][e] * (s * fmaf(g[i][e], 1.f - s, 1.f)));
                 R::set(o, e, r * (dn * w[i][e] - nv * c));
             }
-            store_n<E>(dx + row * D + (i * L + l) * 8, o, cnt[i], true);
-            store_n<E>(dz + row * D + (i * L + l) * 8, oz, cnt[i], true);
+            store_n<E, 8, STREAM>(dx + row * D + (i * L + l) * 8, o, cnt[i], tails);
+            store_n<E, 8, STREAM>(dz + row * D + (i * L + l) * 8, oz, cnt[i], tails);
         }
     }
     // the workgroup's sums of dw: over its rows' lane groups in order
@@ -188,11 +181,18 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
     }
 }
 
-template <typename E, int L, int NV> void launch_cfg(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
+template <typename E, int L, int NV, bool STREAM>
+void launch_stream(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
     if (bwd)
-        norm_held_bwd_kernel<E, L, NV><<<norm_bwd_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+        norm_held_bwd_kernel<E, L, NV, STREAM><<<norm_bwd_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
     else
-        norm_held_kernel<E, L, NV><<<norm_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+        norm_held_kernel<E, L, NV, STREAM><<<norm_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+}
+template <typename E, int L, int NV> void launch_cfg(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
+    if (streams(p, sizeof(E), 4))                      // three tensors and two of codes
+        launch_stream<E, L, NV, true>(p, x8, z8, bwd, st);
+    else
+        launch_stream<E, L, NV, false>(p, x8, z8, bwd, st);
 }
 template <typename E> void launch_e(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
     const Split s = split_of(p.D);

@@ -62,6 +62,43 @@ __device__ __forceinline__ uint32_t pack4(const uint32_t *c) {
     const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0c);
     return lo | hi;
 }
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32u __attribute__((aligned(1)));
+typedef uint16_t u16u __attribute__((aligned(1)));
+// Eight codes of 8 bits, or the first n of them, at any address; S: past the caches.
+template <bool S = false> __device__ __forceinline__ void store_codes(uint8_t *p, uint32_t a, uint32_t b, int n) {
+    if (n == 8) {
+        if constexpr (S)
+            __builtin_nontemporal_store(u32x2{a, b}, (u32x2u *)p);
+        else
+            *(u32x2u *)p = u32x2u{a, b};
+        return;
+    }
+    if (n & 4) {
+        *(u32u *)p = a;
+        a = b;
+    }
+    if (n & 2) {
+        *(u16u *)(p + (n & 4)) = (uint16_t)a;
+        a >>= 16;
+    }
+    if (n & 1) p[n - 1] = (uint8_t)a;
+}
+template <bool S = false> __device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n) {
+    if (n == 8) {
+        if constexpr (S) return __builtin_nontemporal_load((const u32x2u *)p);
+        return *(const u32x2u *)p;
+    }
+    uint32_t a = 0, b = 0;
+    if (n & 1) a = p[n - 1];
+    if (n & 2) a = a << 16 | *(const u16u *)(p + (n & 4));
+    if (n & 4) {
+        b = a;
+        a = *(const u32u *)p;
+    }
+    return u32x2{a, b};
+}
 // Code e of a word of four, as fp32.
 __device__ __forceinline__ float held_byte(uint32_t w, int e) { return (float)(int)(int8_t)(w >> (8 * e)); }
 

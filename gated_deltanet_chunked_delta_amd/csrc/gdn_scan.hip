@@ -531,8 +531,6 @@ template <typename E, int VC, bool HELD, bool STREAM> struct Saved {
     }
     __device__ __forceinline__ float get(int e, int, bool) const { return Vector<E, VC>::get(r, e); }
 };
-typedef uint32_t u32u __attribute__((aligned(1)));
-typedef uint16_t u16u __attribute__((aligned(1)));
 template <typename E, int VC, bool STREAM> struct Saved<E, VC, true, STREAM> {
     uint32_t codes, scales;                            // scales: of the first value's group low, of the last one's high
     __device__ __forceinline__ void clear() { codes = scales = 0; }
