@@ -7,6 +7,8 @@
 // Bound by HBM.  Against the norm that keeps x and z as they are the forward pass
 // writes two bytes more an element (bf16: 8.1 instead of 6) and the backward pass
 // reads two less (8.1 instead of 10); what lives from one to the other is halved.
+#include <algorithm>
+
 #include "gdn_norm_device.h"
 #include "gdn_quant_device.h"
 
@@ -90,11 +92,14 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
     }
 }
 
+// Workgroups of 512 threads: twice the waves of the norm's backward pass for as many
+// rows of partial sums, as there is more arithmetic for fewer bytes.
+constexpr int kBwdThreads = 512;
 template <typename E, int L, int NV, bool STREAM>
-__global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {
+__global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 4 : 2) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {
     typedef Raw8<E> R;
     typedef typename R::T V;
-    constexpr int NT = threads_of(L), GPB = NT / L;
+    constexpr int NT = kBwdThreads, GPB = NT / L;
     __shared__ float red[2][16];
     __shared__ float red2[2][16];
     __shared__ float acc[GPB][L * NV * 8];
@@ -181,10 +186,15 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_bwd_kernel(NormParams
     }
 }
 
+// At most as many as norm_bwd_workspace_bytes has rows for.
+int held_bwd_blocks(int64_t rows, int D) {
+    const int gpb = kBwdThreads / split_of(D).L;
+    return (int)std::min<int64_t>((rows + gpb - 1) / gpb, norm_bwd_blocks(rows, D));
+}
 template <typename E, int L, int NV, bool STREAM>
 void launch_stream(const NormParams &p, const Held &x8, const Held &z8, bool bwd, hipStream_t st) {
     if (bwd)
-        norm_held_bwd_kernel<E, L, NV, STREAM><<<norm_bwd_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
+        norm_held_bwd_kernel<E, L, NV, STREAM><<<held_bwd_blocks(p.rows, p.D), kBwdThreads, 0, st>>>(p, x8, z8);
     else
         norm_held_kernel<E, L, NV, STREAM><<<norm_blocks(p.rows, p.D), threads_of(L), 0, st>>>(p, x8, z8);
 }
@@ -229,7 +239,7 @@ hipError_t launch_norm_held_bwd(const NormParams &p, const Held &x8, const Held 
         if (prof) prof->end(kNormBwdKernel, stream);
         if (err != hipSuccess) return err;
     }
-    return launch_column_sum(p.part, p.rows > 0 ? norm_bwd_blocks(p.rows, p.D) : 0, p.D, p.dweight, p.D, 0, nullptr,
+    return launch_column_sum(p.part, p.rows > 0 ? held_bwd_blocks(p.rows, p.D) : 0, p.D, p.dweight, p.D, 0, nullptr,
                              stream, prof);
 }
 
