@@ -353,6 +353,13 @@ def _held_rows(c, rows, D, dev, name):
     return (codes, scales), gdn_held(codes.data_ptr(), scales.data_ptr())
 
 
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU device (there is no CPU path)")
+    return dev
+
+
 def _new_checkpoint(x):
     dims = x.shape
     codes = torch.empty(dims, dtype=torch.int8, device=x.device)
@@ -393,9 +400,7 @@ def restore_activation(checkpoint, dtype=torch.bfloat16, out=None):
         raise ValueError("dtype must be bfloat16 or float32")
     if codes.dim() == 0 or not 0 < codes.shape[-1] < 1 << 31:
         raise ValueError("codes must be [...,D], 0 < D < 2^31")
-    dev = codes.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on a GPU device (there is no CPU path)")
+    dev = _device(codes)
     D = codes.shape[-1]
     n = codes.numel() // D
     if n >> 31:
