@@ -206,7 +206,7 @@ def gated_linear_recurrence(x, g, beta=None, initial_state=None, output_final_st
     D = shape.D
     lib = _lib or _load()
     if out is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x)          # contiguous: x is, or its rows lie apart
     else:
         y = _given(out, x.shape, x, dev, "out")
         _apart("out", [y], x, g, beta, initial_state, state_pool)
@@ -228,7 +228,7 @@ def gated_linear_recurrence(x, g, beta=None, initial_state=None, output_final_st
     if not output_final_state:
         final_state = None
     elif final_state is None:
-        final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        final_state = x.new_empty((N, D), dtype=torch.float32) if initial_state is None else torch.empty_like(initial_state)
     else:
         if final_state.shape != (N, D) or final_state.dtype != torch.float32 or not final_state.is_contiguous() \
                 or final_state.get_device() != dev:
@@ -265,7 +265,7 @@ def gated_linear_recurrence_steps(x, g, state_pool, state_indices, beta=None, cu
         raise ValueError("state_pool must be float32 or bfloat16")
     pool, kept = _step_pool(dev, state_pool, state_indices, num_accepted, N, (shape.D,), "state_pool")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x)
     else:
         _apart("out", [_given(out, x.shape, x, dev, "out")], x, g, beta, state_pool)
     _run(dev, (_lib or _load()).gdn_scan_steps, x.data_ptr(), g.data_ptr(), _p(beta), _addr(pool), _p(cu),
@@ -329,9 +329,9 @@ def gated_linear_recurrence_bwd(x, g, y, dy, beta=None, dht=None, initial_state=
     lib = _lib or _load()
     wp, wb, ws = _scratch(workspace, lib.gdn_scan_workspace_bytes(_addr(shape), 1), dev, dy)
     dx = torch.empty_like(dy)
-    dg = torch.empty(dims, dtype=g.dtype, device=dy.device)
+    dg = torch.empty_like(dy, dtype=g.dtype)
     dbeta = None if beta is None else torch.empty_like(dg)
-    dinitial = torch.empty((N, D), dtype=torch.float32, device=dy.device) if output_dinitial else None
+    dinitial = dy.new_empty((N, D), dtype=torch.float32) if output_dinitial else None
     _run(dev, lib.gdn_scan_bwd, xp, g.data_ptr(), _p(beta), yp, _r(x8), _r(y8), dy.data_ptr(), _p(dht),
          _p(initial_state), _p(cu_seqlens), dx.data_ptr(), dg.data_ptr(), _p(dbeta), _p(dinitial), _addr(shape), wp, wb)
     return dx, dg, dbeta, dinitial
@@ -362,8 +362,8 @@ def _device(t):
 
 def _new_checkpoint(x):
     dims = x.shape
-    codes = torch.empty(dims, dtype=torch.int8, device=x.device)
-    return Checkpoint(codes, torch.empty((*dims[:-1], -(-dims[-1] // GROUP)), dtype=torch.bfloat16, device=x.device))
+    return Checkpoint(x.new_empty(dims, dtype=torch.int8),
+                      x.new_empty((*dims[:-1], -(-dims[-1] // GROUP)), dtype=torch.bfloat16))
 
 
 def checkpoint_activation(x):

@@ -103,16 +103,21 @@ template <int VC> __device__ __forceinline__ void store_states(void *s, int64_t 
 }
 // ---------------------------------------------------------------------------
 // Tiles.  The tokens of all sequences lie on one axis, which is cut into tiles of
-// W * S tokens; a workgroup of W waves takes one tile of up to 64 * VC channels,
-// every wave S of its tokens, every lane VC channels.  All of it is loaded once,
-// into registers; what a wave's tokens do to a state is h -> A h + b, and such maps
-// compose.  The backward pass is the same with tiles, waves and tokens in reverse.
+// W * R * S tokens; a workgroup of W waves takes one tile of up to 64 / R * VC
+// channels, every strip of 64 / R lanes S of its tokens, every lane VC channels.  All
+// of it is loaded once, into registers; what a strip's tokens do to a state is
+// h -> A h + b, and such maps compose.  The backward pass is the same with tiles,
+// strips and tokens in reverse.  R = 1, and 4 for up to 64 channels, which a wave
+// has not lanes enough for otherwise.
 // ---------------------------------------------------------------------------
 constexpr int kGroupTiles = 8, kBlockGroups = 8;   // tiles of a group, groups of a block
 
+// What is the same in all lanes of a strip, as a scalar where the strip is the wave.
+template <int R> __device__ __forceinline__ int strip_int(int x) { return R == 1 ? __builtin_amdgcn_readfirstlane(x) : x; }
+
 // Channels of a lane.  The vectors of VC channels are shared out evenly among the
 // column blocks; the last one of an odd row ends with it and overlaps its neighbour,
-// which is in the same wave: both compute and store the same values.
+// which is in the same strip: both compute and store the same values.
 struct Lane {
     int c;
     bool live;
@@ -138,9 +143,9 @@ __host__ __device__ __forceinline__ int64_t handed_words(int64_t tiles, int64_t 
     return 2 + (tiles + groups + (groups + kBlockGroups - 1) / kBlockGroups) * row;
 }
 // The words of column block cb, this lane's first.
-template <int VC> __device__ __forceinline__ Handed handed_of(void *ws, int64_t tiles, int ncb, int cb, int lane) {
-    const int64_t row = (int64_t)ncb * VC * 64;
-    unsigned long long *w = (unsigned long long *)ws + 2 + cb * VC * 64 + lane;
+template <int VC, int LR> __device__ __forceinline__ Handed handed_of(void *ws, int64_t tiles, int ncb, int cb, int lane) {
+    const int64_t row = (int64_t)ncb * VC * LR;
+    unsigned long long *w = (unsigned long long *)ws + 2 + cb * VC * LR + lane;
     return {w, w + tiles * row, w + (tiles + groups_of(tiles)) * row, row};
 }
 
@@ -151,13 +156,13 @@ __device__ __forceinline__ void put(unsigned long long *w, float A, float h) {
     __hip_atomic_store(w, (unsigned long long)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(h),
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-template <int VC> __device__ __forceinline__ void await(const unsigned long long *w, float2 (*to)[64]) {
+template <int VC, int LR> __device__ __forceinline__ void await(const unsigned long long *w, float2 (*to)[LR]) {
     unsigned long long v[VC];
     for (;;) {
         bool all = true;
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            v[e] = __hip_atomic_load(w + e * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v[e] = __hip_atomic_load(w + e * LR, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             all = all && (long long)v[e] < 0;
         }
         if (all) break;
@@ -245,12 +250,13 @@ __device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, i
 }
 
 // Sequence of the token before token i of the tile (of the tile's first where i = 0).
-template <int TT> __device__ __forceinline__ int sequence_before(const Sequences<TT> &q, int i, int lane) {
+template <int R, int TT> __device__ __forceinline__ int sequence_before(const Sequences<TT> &q, int i, int lane) {
+    constexpr int LR = 64 / R;
     int n = q.first;
-    for (int j = lane; j < i; j += 64) n = max(n, q.start[j]);
+    for (int j = lane; j < i; j += LR) n = max(n, q.start[j]);
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) n = max(n, __shfl_xor(n, o));
-    return __builtin_amdgcn_readfirstlane(n);
+    for (int o = LR / 2; o >= 1; o >>= 1) n = max(n, __shfl_xor(n, o));
+    return strip_int<R>(n);
 }
 
 // Tiles are taken in the order of a counter, so that whatever tile a workgroup waits
@@ -263,26 +269,27 @@ __device__ __forceinline__ int next_tile(void *ws, int tiles, int *ticket) {
     return __builtin_amdgcn_readfirstlane(*ticket);
 }
 
-template <int VC, int W> struct Exchange {
-    float2 maps[W][VC][64];                            // what each wave's tokens do to a state
-    float2 before[kGroupTiles + kBlockGroups - 1][VC][64];   // tiles and groups before this tile, the state before them
-    int cut[W];                                        // a state begins anew in the wave's tokens
+template <int VC, int W, int R> struct Exchange {
+    static constexpr int LR = 64 / R;                  // lanes of a strip
+    float2 maps[W * R][VC][LR];                        // what each strip's tokens do to a state
+    float2 before[kGroupTiles + kBlockGroups - 1][VC][LR];   // tiles and groups before this tile, the state before them
+    int cut[W * R];                                    // a state begins anew in the strip's tokens
 };
-// Maps lo .. hi - 1 of those that a tile waits for, one a wave: nt of tiles from `from`
+// Maps lo .. hi - 1 of those that a tile waits for, one a strip: nt of tiles from `from`
 // on, ng of groups from gfrom on, the state before the block.
-template <int VC, int W>
-__device__ __forceinline__ void fetch(Exchange<VC, W> &x, const Handed &hand, int lane, int rank, int lo, int hi, int from,
+template <int VC, int W, int R>
+__device__ __forceinline__ void fetch(Exchange<VC, W, R> &x, const Handed &hand, int lane, int rank, int lo, int hi, int from,
                                       int nt, int gfrom, int ng, int block) {
 #pragma unroll 1
-    for (int k = lo + rank; k < hi; k += W) {
+    for (int k = lo + rank; k < hi; k += W * R) {
         const unsigned long long *src = k < nt        ? hand.tiles + (from + k) * hand.row
                                         : k < nt + ng ? hand.groups + (gfrom + k - nt) * hand.row
                                                       : hand.states + block * hand.row;
-        await<VC>(src, (float2 (*)[64])&x.before[k][0][lane]);
+        await<VC, 64 / R>(src, (float2 (*)[64 / R])&x.before[k][0][lane]);
     }
 }
-// The state that comes into a wave's tokens.  rank: the wave's place in its tile, tile:
-// the tile's place in the order of the pass; A, b: the wave's map, fresh: whether a
+// The state that comes into a strip's tokens.  rank: the strip's place in its tile, tile:
+// the tile's place in the order of the pass; A, b: the strip's map, fresh: whether a
 // state begins anew in it (its map is then b alone); waits: whether a state comes
 // into the tile, since: the place of the tile where it began.
 //
@@ -292,14 +299,14 @@ __device__ __forceinline__ void fetch(Exchange<VC, W> &x, const Handed &hand, in
 // group's map, the last one of a block the state.  A state handed on from one
 // workgroup to another takes 2.8 us (a store, a load that meets it, the sum between);
 // with one level, from group to group, 131,072 tokens of 256 channels took 700 us.
-template <int VC, int W>
-__device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand, int lane, int rank, int tile, int tiles,
+template <int VC, int W, int R>
+__device__ __forceinline__ void carry_in(Exchange<VC, W, R> &x, const Handed &hand, int lane, int rank, int tile, int tiles,
                                          bool waits, int since, bool fresh, const float *A, const float *b, float *h) {
 #pragma unroll
     for (int e = 0; e < VC; ++e) x.maps[rank][e][lane] = float2{A[e], b[e]};
     if (lane == 0) x.cut[rank] = fresh;
     lds_barrier();
-    bool own = false;                                  // the state began in the tile, before the wave
+    bool own = false;                                  // the state began in the tile, before the strip
     float Ae[VC], he[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
@@ -317,11 +324,11 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
             Ae[e] *= m.x;
         }
     }
-    const bool last = rank == W - 1;                   // the wave whose end is the tile's
+    const bool last = rank == W * R - 1;               // the strip whose end is the tile's
     if (tiles > 1 && last) {
 #pragma unroll
         for (int e = 0; e < VC; ++e)
-            put(hand.tiles + tile * hand.row + e * 64, Ae[e] * A[e], fresh ? b[e] : fmaf(A[e], he[e], b[e]));
+            put(hand.tiles + tile * hand.row + e * (64 / R), Ae[e] * A[e], fresh ? b[e] : fmaf(A[e], he[e], b[e]));
     }
     const int group = tile / kGroupTiles, base = group * kGroupTiles, block = group / kBlockGroups;
     const int from = max(base, since), nt = waits ? tile - from : 0;
@@ -336,7 +343,7 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
         ht[e] = hin[e] = 0.f;
     }
     if (waits) {
-        fetch<VC, W>(x, hand, lane, rank, 0, ends_group ? nt : all, from, nt, gfrom, ng, block);
+        fetch<VC, W, R>(x, hand, lane, rank, 0, ends_group ? nt : all, from, nt, gfrom, ng, block);
         lds_barrier();
 #pragma unroll 1
         for (int k = 0; k < nt; ++k)
@@ -351,12 +358,12 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
             const float T = Ae[e] * A[e], v = fresh ? b[e] : fmaf(A[e], he[e], b[e]);
-            put(hand.groups + group * hand.row + e * 64, At[e] * T, fresh || own ? v : fmaf(T, ht[e], v));
+            put(hand.groups + group * hand.row + e * (64 / R), At[e] * T, fresh || own ? v : fmaf(T, ht[e], v));
         }
     }
     if (waits) {
         if (ends_group) {
-            fetch<VC, W>(x, hand, lane, rank, nt, all, from, nt, gfrom, ng, block);
+            fetch<VC, W, R>(x, hand, lane, rank, nt, all, from, nt, gfrom, ng, block);
             lds_barrier();
         }
         if (further)
@@ -377,25 +384,26 @@ __device__ __forceinline__ void carry_in(Exchange<VC, W> &x, const Handed &hand,
     if (ends_group && group % kBlockGroups == kBlockGroups - 1 && last) {
 #pragma unroll
         for (int e = 0; e < VC; ++e)
-            put(hand.states + (block + 1) * hand.row + e * 64, 0.f, fresh ? b[e] : fmaf(A[e], h[e], b[e]));
+            put(hand.states + (block + 1) * hand.row + e * (64 / R), 0.f, fresh ? b[e] : fmaf(A[e], h[e], b[e]));
     }
 }
 
-template <typename E, typename G, bool BETA, bool STREAM, int VC, int W, int S>
+template <typename E, typename G, bool BETA, bool STREAM, int VC, int W, int S, int R>
 __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, int tiles) {
-    constexpr int NT = W * 64, TT = W * S;
+    constexpr int NT = W * 64, LR = 64 / R, TT = W * R * S;
+    static_assert(S <= LR, "a strip looks at its tokens with a lane each");
     __shared__ Sequences<TT> q;
-    __shared__ Exchange<VC, W> x;
+    __shared__ Exchange<VC, W, R> x;
     __shared__ int ticket;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x % LR, w = strip_int<R>(threadIdx.x / LR);   // in the strip; the strip
     const int id = next_tile(p.ws, tiles, &ticket);
-    const Handed hand = handed_of<VC>(p.ws, tiles, ncb, id % ncb, lane);
+    const Handed hand = handed_of<VC, LR>(p.ws, tiles, ncb, id % ncb, lane);
     const int tile = id / ncb, t0 = tile * TT;
     const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
     const int t_end = p.cu_seqlens ? cu_at(p.cu_seqlens, p.N, p.T_tot) : p.T_tot;
     empty_sequences<VC, W>(p, tile, tiles, ln.c, ln.live);
     if (t0 >= t_end) return;
-    const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the wave's tokens
+    const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the strip's tokens
 
     typedef Vector<E, VC> RE;
     typedef Vector<G, VC> RG;
@@ -438,11 +446,13 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
             uv = u[s][e];
         }
     };
-    // sequences that begin at, or end with, the wave's tokens
+    // sequences that begin at, or end with, the strip's tokens
     const bool is = lane < nv;
     const int at = w * S + min(lane, S - 1);
-    const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
-    const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
+    const int strip = threadIdx.x % 64 / LR * LR;      // its first lane
+    const uint32_t mask = LR == 64 ? ~0u : (1u << (LR % 32)) - 1;
+    const uint32_t starts = (uint32_t)(__ballot(is && q.start[at] >= 0) >> strip) & mask;
+    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end)) >> strip) & mask;
     auto initial = [&](int n, float *h) {
         int64_t from = (int64_t)n * p.D + ln.c;
         bool has = p.initial != nullptr && ln.live;
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (starts >> s & 1) {                         // what came in is replaced
-            initial(__builtin_amdgcn_readfirstlane(q.start[w * S + s]), h0);
+            initial(strip_int<R>(q.start[w * S + s]), h0);
 #pragma unroll
             for (int e = 0; e < VC; ++e) b[e] = h0[e];
         }
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
             A[e] *= av;
         }
     }
-    carry_in<VC, W>(x, hand, lane, w, tile, tiles, q.first_token < t0, q.first_token / TT, starts != 0, A, b, h);
+    carry_in<VC, W, R>(x, hand, lane, w, tile, tiles, q.first_token < t0, q.first_token / TT, starts != 0, A, b, h);
     if constexpr (RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -485,14 +495,14 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
             if (BETA) forget(br[s]);
         }
     E *y = (E *)p.y + (int64_t)tw * p.D + ln.c;
-    int seq = ends ? sequence_before(q, w * S, lane) : 0;
+    int seq = ends ? sequence_before<R>(q, w * S, lane) : 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (starts >> s & 1) {
-            // The last sequence that begins here may end with another wave, which may have
+            // The last sequence that begins here may end with another strip, which may have
             // stored its final state where its initial state was: that one is h0 still.
             // The others end here.
-            seq = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+            seq = strip_int<R>(q.start[w * S + s]);
             if (starts >> s != 1)
                 initial(seq, h);
             else
@@ -547,15 +557,16 @@ template <typename E, int VC, bool STREAM> struct Saved<E, VC, true, STREAM> {
     }
 };
 
-template <typename E, typename G, bool BETA, bool HELD, bool STREAM, int VC, int W, int S>
+template <typename E, typename G, bool BETA, bool HELD, bool STREAM, int VC, int W, int S, int R>
 __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int ncb, int tiles) {
-    constexpr int NT = W * 64, TT = W * S;
+    constexpr int NT = W * 64, LR = 64 / R, TT = W * R * S;
+    static_assert(S <= LR, "a strip looks at its tokens with a lane each");
     __shared__ Sequences<TT> q;
-    __shared__ Exchange<VC, W> x;
+    __shared__ Exchange<VC, W, R> x;
     __shared__ int ticket;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x % LR, w = strip_int<R>(threadIdx.x / LR);   // in the strip; the strip
     const int id = next_tile(p.ws, tiles, &ticket);
-    const Handed hand = handed_of<VC>(p.ws, tiles, ncb, id % ncb, lane);
+    const Handed hand = handed_of<VC, LR>(p.ws, tiles, ncb, id % ncb, lane);
     const int place = id / ncb, tile = tiles - 1 - place, t0 = tile * TT;
     const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
     const int t_end = p.cu_seqlens ? cu_at(p.cu_seqlens, p.N, p.T_tot) : p.T_tot;
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
         empty_sequences<VC, W>(e, tile, tiles, ln.c, ln.live);
     }
     if (t0 >= t_end) return;
-    const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the wave's tokens
+    const int tw = t0 + w * S, nv = min(max(t_end - tw, 0), S);   // the strip's tokens
     const bool two = p.D % VC != 0;
 
     typedef Vector<E, VC> RE;
@@ -619,13 +630,15 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     }
     const bool is = lane < nv;
     const int at = w * S + min(lane, S - 1);
-    const uint32_t starts = (uint32_t)__ballot(is && q.start[at] >= 0);
-    const uint32_t ends = (uint32_t)__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end));
-    const int seq = ends ? sequence_before(q, w * S, lane) : 0;   // of the wave's first token, unless one begins with it
+    const int strip = threadIdx.x % 64 / LR * LR;      // its first lane
+    const uint32_t mask = LR == 64 ? ~0u : (1u << (LR % 32)) - 1;
+    const uint32_t starts = (uint32_t)(__ballot(is && q.start[at] >= 0) >> strip) & mask;
+    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end)) >> strip) & mask;
+    const int seq = ends ? sequence_before<R>(q, w * S, lane) : 0;   // of the wave's first token, unless one begins with it
     // the gradient of the final state of the sequence that ends with token s
     auto final_gradient = [&](int s, float *c) {
         const uint32_t up_to = starts & ((2u << s) - 1);
-        const int n = up_to ? __builtin_amdgcn_readfirstlane(q.start[w * S + 31 - __builtin_clz(up_to)]) : seq;
+        const int n = up_to ? strip_int<R>(q.start[w * S + 31 - __builtin_clz(up_to)]) : seq;
 #pragma unroll
         for (int e = 0; e < VC; ++e) c[e] = 0.f;
         if (p.dht && ln.live) load_states<VC>(p.dht, (int64_t)n * p.D + ln.c, 0, c);
@@ -647,10 +660,10 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
         }
     }
     // whether a gradient comes into the tile, and from where on
-    const int count = min(TT, t_end - t0), last = sequence_before(q, count, lane);
+    const int count = min(TT, t_end - t0), last = sequence_before<R>(q, count, lane);
     const bool waits = q.start[count] < 0 && t0 + count < t_end;
     const int end = p.cu_seqlens ? min(cu_at(p.cu_seqlens, last + 1, p.T_tot), t_end) : (last + 1) * p.T;
-    carry_in<VC, W>(x, hand, lane, W - 1 - w, place, tiles, waits, tiles - 1 - (max(end, t0 + count) - 1) / TT, ends != 0, A, b, c);
+    carry_in<VC, W, R>(x, hand, lane, W * R - 1 - w, place, tiles, waits, tiles - 1 - (max(end, t0 + count) - 1) / TT, ends != 0, A, b, c);
     if constexpr (RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -664,7 +677,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
         int n = 0;
         float h0[VC];
         if (first) {
-            n = __builtin_amdgcn_readfirstlane(q.start[w * S + s]);
+            n = strip_int<R>(q.start[w * S + s]);
 #pragma unroll
             for (int e = 0; e < VC; ++e) h0[e] = 0.f;
             if (p.initial && ln.live) load_states<VC>(p.initial, (int64_t)n * p.D + ln.c, 0, h0);
@@ -757,19 +770,24 @@ template <typename E, typename G, bool BETA> void launch_steps_vc(const ScanPara
 }
 
 enum Pass { kForward, kBackward, kSteps };
-// Channels of a lane, waves of a workgroup and tokens of a wave, for at least two
-// workgroups a CU (128 registers a lane) and few tiles to hand states through.
+// Channels of a lane, waves of a workgroup, tokens of a strip and strips of a wave, for
+// at least two workgroups a CU (128 registers a lane) and few tiles to hand states
+// through.
 struct Tile {
-    int VC, W, S;
+    int VC, W, S, R;
+    constexpr int tokens() const { return W * R * S; }
 };
-constexpr Tile tile_of(bool gate_f32, bool backward, bool beta, bool held) {
-    if (backward) return gate_f32 ? Tile{4, 8, 4} : beta && !held ? Tile{2, 8, 16} : Tile{4, 8, 8};
-    return gate_f32 ? Tile{4, 8, 8} : Tile{2, 8, 16};
+// By the number of channels: one a lane below 4, four strips a wave up to 64.
+enum Width { kOne, kNarrow, kWide };
+Width width_of(int D) { return D < 4 ? kOne : D <= 64 ? kNarrow : kWide; }
+constexpr Tile tile_of(Width width, bool gate_f32, bool backward, bool beta, bool held) {
+    if (width != kWide) return {width == kOne ? 1 : 4, 8, backward && gate_f32 ? 4 : 8, 4};
+    if (backward) return gate_f32 ? Tile{4, 8, 4, 1} : beta && !held ? Tile{2, 8, 16, 1} : Tile{4, 8, 8, 1};
+    return gate_f32 ? Tile{4, 8, 8, 1} : Tile{2, 8, 16, 1};
 }
-// Rows of fewer channels than a lane's have one a lane.
-constexpr Tile narrow(Tile t) { return {1, t.W, t.S}; }
-int tiles_of(int64_t T_tot, const Tile &t) { return (int)std::max<int64_t>((T_tot + t.W * t.S - 1) / (t.W * t.S), 1); }
-int blocks_of(int D, const Tile &t) { return t.VC == 1 ? column_blocks<1>(D) : t.VC == 2 ? column_blocks<2>(D) : column_blocks<4>(D); }
+int tiles_of(int64_t T_tot, const Tile &t) { return (int)std::max<int64_t>((T_tot + t.tokens() - 1) / t.tokens(), 1); }
+int blocks_of(int D, const Tile &t) { return t.R > 1 ? 1 : t.VC == 2 ? column_blocks<2>(D) : column_blocks<4>(D); }
+int64_t row_words(int D, const Tile &t) { return (int64_t)blocks_of(D, t) * t.VC * (64 / t.R); }
 
 // Passes over more than the 256 MiB of the last cache are streamed past it.
 template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
@@ -777,39 +795,42 @@ template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
     const int token = pass == kForward ? 2 * sizeof(E) + gates * sizeof(G) : 2 * sizeof(E) + 2 * gates * sizeof(G) + kept;
     return (int64_t)p.T_tot * p.D * token > 256 << 20;
 }
-template <typename E, typename G, bool BETA, bool HELD, bool NARROW> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
-    constexpr bool f32 = sizeof(G) == 4;
-    constexpr Tile f = NARROW ? narrow(tile_of(f32, false, BETA, HELD)) : tile_of(f32, false, BETA, HELD);
-    constexpr Tile b = NARROW ? narrow(tile_of(f32, true, BETA, HELD)) : tile_of(f32, true, BETA, HELD);
+template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
+    constexpr Tile f = tile_of(WIDTH, sizeof(G) == 4, false, BETA, HELD), b = tile_of(WIDTH, sizeof(G) == 4, true, BETA, HELD);
+    constexpr bool wide = WIDTH == kWide;
     const Tile t = pass == kForward ? f : b;
     const int tiles = tiles_of(p.T_tot, t), ncb = blocks_of(p.D, t);
     if (tiles > 1) {
-        const int64_t n = handed_words(tiles, (int64_t)ncb * t.VC * 64) / 2;
+        const int64_t n = handed_words(tiles, row_words(p.D, t)) / 2;
         clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>((uint4 *)p.ws, n);
     }
     const unsigned grid = (unsigned)(tiles * ncb);
-    const bool stream = !NARROW && streams<E, G>(p, pass);
+    const bool stream = wide && streams<E, G>(p, pass);
     if (pass == kBackward) {
         if (stream)
-            scan_bwd_kernel<E, G, BETA, HELD, !NARROW, b.VC, b.W, b.S><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
+            scan_bwd_kernel<E, G, BETA, HELD, wide, b.VC, b.W, b.S, b.R><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
         else
-            scan_bwd_kernel<E, G, BETA, HELD, false, b.VC, b.W, b.S><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
+            scan_bwd_kernel<E, G, BETA, HELD, false, b.VC, b.W, b.S, b.R><<<grid, b.W * 64, 0, st>>>(p, ncb, tiles);
     } else if constexpr (!HELD) {
         if (stream)
-            scan_kernel<E, G, BETA, !NARROW, f.VC, f.W, f.S><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
+            scan_kernel<E, G, BETA, wide, f.VC, f.W, f.S, f.R><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
         else
-            scan_kernel<E, G, BETA, false, f.VC, f.W, f.S><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
+            scan_kernel<E, G, BETA, false, f.VC, f.W, f.S, f.R><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
     }
 }
-template <typename E, typename G, bool HELD> void launch_vc(const ScanParams &p, Pass pass, hipStream_t st) {
-    if (p.D < tile_of(sizeof(G) == 4, pass == kBackward, p.beta != nullptr, HELD).VC)
-        p.beta ? launch_tiles<E, G, true, HELD, true>(p, pass, st) : launch_tiles<E, G, false, HELD, true>(p, pass, st);
-    else
-        p.beta ? launch_tiles<E, G, true, HELD, false>(p, pass, st) : launch_tiles<E, G, false, HELD, false>(p, pass, st);
+template <typename E, typename G, bool BETA, bool HELD> void launch_width(const ScanParams &p, Pass pass, hipStream_t st) {
+    switch (width_of(p.D)) {
+        case kOne: return launch_tiles<E, G, BETA, HELD, kOne>(p, pass, st);
+        case kNarrow: return launch_tiles<E, G, BETA, HELD, kNarrow>(p, pass, st);
+        case kWide: return launch_tiles<E, G, BETA, HELD, kWide>(p, pass, st);
+    }
+}
+template <typename E, typename G, bool HELD> void launch_beta(const ScanParams &p, Pass pass, hipStream_t st) {
+    p.beta ? launch_width<E, G, true, HELD>(p, pass, st) : launch_width<E, G, false, HELD>(p, pass, st);
 }
 template <typename E, typename G> void launch_e(const ScanParams &p, Pass pass, hipStream_t st) {
     if (pass != kSteps) {
-        p.y8.codes ? launch_vc<E, G, true>(p, pass, st) : launch_vc<E, G, false>(p, pass, st);
+        p.y8.codes ? launch_beta<E, G, true>(p, pass, st) : launch_beta<E, G, false>(p, pass, st);
         return;
     }
     p.beta ? launch_steps_vc<E, G, true>(p, st) : launch_steps_vc<E, G, false>(p, st);
@@ -832,24 +853,21 @@ hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, h
 }  // namespace
 
 // Over the tiles that calls of these sizes and types take: f(tile).
-template <typename F> void each_tile(int64_t D, int gate_f32, bool backward, F f) {
-    for (int i = 0; i < 4; ++i) {
-        const Tile t = tile_of(gate_f32 != 0, backward, i & 1, i & 2);
-        f(D < t.VC ? narrow(t) : t);
-    }
+template <typename F> void each_tile(int D, int gate_f32, bool backward, F f) {
+    for (int i = 0; i < 4; ++i) f(tile_of(width_of(D), gate_f32 != 0, backward, i & 1, i & 2));
 }
 size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward) {
     size_t most = 0;
     each_tile(D, gate_f32, backward, [&](const Tile &t) {
         const int tiles = tiles_of(T_tot, t);
-        if (tiles > 1) most = std::max(most, (size_t)handed_words(tiles, (int64_t)blocks_of(D, t) * t.VC * 64) * 8);
+        if (tiles > 1) most = std::max(most, (size_t)handed_words(tiles, row_words(D, t)) * 8);
     });
     return most;
 }
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N) {
     int64_t most = N * steps_blocks((int)D);
     for (int i = 0; i < 4; ++i)
-        each_tile(D, i & 1, i & 2, [&](const Tile &t) { most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t)); });
+        each_tile((int)D, i & 1, i & 2, [&](const Tile &t) { most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t)); });
     return most;
 }
 

@@ -69,6 +69,14 @@ CASES = {   # lengths (a tuple: equal), D, beta, initial state, extra columns of
     "border_rows": ((256,) * 5, 257, True, True, 0),
     "long_packed": ([3, 900, 0, 2500, 1, 64, 511], 18, True, True, 2),
     "wide": ((33,), 5000, True, False, 0),
+    # states handed on over several blocks of 64 tiles
+    "blocks": ((36000,), 5, True, True, 0),
+    "blocks_rows": ((17500, 17500), 64, False, True, 0),
+    "blocks_packed": ([40, 17000, 1, 0, 9000, 9000], 66, True, True, 2),
+    "sixty_five": ([300, 700], 65, True, True, 0),
+    "sixteen": ([5, 1, 900, 33], 16, True, True, 0),
+    "two_channels": ((700, 700), 2, True, True, 1),
+    "four_channels": ([1, 2, 700], 4, False, True, 0),
 }
 
 
@@ -106,7 +114,7 @@ def test_recurrence_matches_the_definition(name, dtype, gate):
     _near("y", y, ref, mag, 5)
     _near("final", final, fin, mfin, 5)
     # no final state; the given buffers; the initial state's buffer updated in place; the same bits again
-    out, ws = torch.empty_like(y), torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)
+    out, ws = torch.empty_like(y), torch.full((1 << 23,), 255, dtype=torch.uint8, device=DEV)
     y2, none = gdn.gated_linear_recurrence(*args, initial_state=x["h0"], cu_seqlens=x["cu"], output_final_state=False,
                                            out=out, workspace=ws)
     assert none is None and y2 is out and torch.equal(y2, y)
@@ -138,7 +146,7 @@ def test_recurrence_backward_matches_the_definition(name, dtype, gate):
         _near("dbeta", dbeta, *ref["dbeta"], 8)
     if dinitial is not None:
         _near("dinitial", dinitial, *ref["dinitial"], 8)
-    again = call(workspace=torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV))
+    again = call(workspace=torch.full((1 << 23,), 255, dtype=torch.uint8, device=DEV))
     assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, again))
 
 
