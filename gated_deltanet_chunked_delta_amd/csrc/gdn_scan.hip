@@ -119,13 +119,19 @@ template <int R> __device__ __forceinline__ int strip_int(int x) { return R == 1
 // column blocks; the last one of an odd row ends with it and overlaps its neighbour,
 // which is in the same strip: both compute and store the same values.
 struct Lane {
-    int c;
+    uint32_t c;                                        // unsigned: a 32-bit offset from a row in scalar registers
     bool live;
 };
+template <typename E> __device__ __forceinline__ const E *at(const void *base, int64_t row, int64_t stride, uint32_t c) {
+    return (const E *)((const char *)((const E *)base + row * stride) + c * (uint32_t)sizeof(E));
+}
+template <typename E> __device__ __forceinline__ E *at(void *base, int64_t row, int64_t stride, uint32_t c) {
+    return (E *)((char *)((E *)base + row * stride) + c * (uint32_t)sizeof(E));
+}
 template <int VC> __device__ __forceinline__ Lane lane_of(int D, int ncb, int cb, int lane) {
     const int nv = (D + VC - 1) / VC, each = nv / ncb, more = nv % ncb;
     const int v = cb * each + min(cb, more) + lane;
-    return {min(v * VC, D - VC), lane < each + (cb < more ? 1 : 0)};
+    return {(uint32_t)min(v * VC, D - VC), lane < each + (cb < more ? 1 : 0)};
 }
 template <int VC> __host__ __device__ __forceinline__ int column_blocks(int D) { return ((D + VC - 1) / VC + 63) / 64; }
 
@@ -228,7 +234,7 @@ __device__ __forceinline__ void find_sequences(Sequences<TT> &q, const ScanParam
 // Rows of sequences without tokens, shared out over the tiles: the final state is the
 // initial one.
 template <int VC, int W>
-__device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, int tiles, int c, bool live) {
+__device__ __forceinline__ void empty_sequences(const ScanParams &p, int tile, int tiles, uint32_t c, bool live) {
     if (!p.final_state || (p.indices && p.initial) || !live) return;   // a pool's slots keep what they hold
     const int lo = (int)((int64_t)p.N * tile / tiles), hi = (int)((int64_t)p.N * (tile + 1) / tiles);
     for (int n = lo + (threadIdx.x >> 6); n < hi; n += W) {
@@ -407,52 +413,53 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
 
     typedef Vector<E, VC> RE;
     typedef Vector<G, VC> RG;
-    // bf16 gates stay as they were loaded and their decays are taken twice (2 or 3
-    // registers a token and two channels instead of 4); others become decays and inputs
+    // Inputs stay as they were loaded where that takes fewer registers (bf16 gates), and
+    // are widened twice; decays are taken once.
     constexpr bool RAW = sizeof(G) == 2;
     typename RE::T xr[S];
     typename RG::T gr[S], br[S];
-    float a[RAW ? 1 : S][VC], u[RAW ? 1 : S][VC];
-    const E *xp = (const E *)p.x + (int64_t)tw * p.x_stride;
-    const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
+    float a[S][VC], u[RAW ? 1 : S][VC];
+    // every lane loads, those without channels another's and those without tokens the
+    // last token, so that the loads are issued in one run
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        xr[s] = RE::zero();
-        gr[s] = RG::zero();                            // a = 1, u = 0: the state stays
-        if (BETA) br[s] = RG::zero();
-        if (s < nv && ln.live) {
-            xr[s] = RE::template load<STREAM>(xp + s * p.x_stride + ln.c);
-            gr[s] = RG::template load<STREAM>(gp + s * p.g_stride + ln.c);
-            if (BETA) br[s] = RG::template load<STREAM>(bp + s * p.beta_stride + ln.c);
-        }
+        const int row = min(tw + s, t_end - 1);
+        xr[s] = RE::template load<STREAM>(at<E>(p.x, row, p.x_stride, ln.c));
+        gr[s] = RG::template load<STREAM>(at<G>(p.g, row, p.g_stride, ln.c));
+        if (BETA) br[s] = RG::template load<STREAM>(at<G>(p.beta, row, p.beta_stride, ln.c));
     }
     find_sequences<TT, NT>(q, p, t0, t_end);
-    if constexpr (!RAW)
+    if (nv < S)                                        // no token: a = 1, u = 0, the state stays
 #pragma unroll
         for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                a[s][e] = decay(RG::get(gr[s], e));
-                u[s][e] = RE::get(xr[s], e);
-                if (BETA) u[s][e] *= RG::get(br[s], e);
+            if (s >= nv) {
+                xr[s] = RE::zero();
+                gr[s] = RG::zero();
             }
-    auto token = [&](int s, int e, float &av, float &uv) {
-        if constexpr (RAW) {
-            av = decay(RG::get(gr[s], e));
-            uv = RE::get(xr[s], e);
-            if (BETA) uv *= RG::get(br[s], e);
-        } else {
-            av = a[s][e];
-            uv = u[s][e];
+    auto input = [&](int s, int e) {
+        const float v = RE::get(xr[s], e);
+        return BETA ? v * RG::get(br[s], e) : v;
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            a[s][e] = decay(RG::get(gr[s], e));
+            if constexpr (!RAW) u[s][e] = input(s, e);
         }
+    auto taken = [&](int s, int e) {
+        if constexpr (RAW)
+            return input(s, e);
+        else
+            return u[s][e];
     };
     // sequences that begin at, or end with, the strip's tokens
     const bool is = lane < nv;
-    const int at = w * S + min(lane, S - 1);
+    const int mine = w * S + min(lane, S - 1);
     const int strip = threadIdx.x % 64 / LR * LR;      // its first lane
     const uint32_t mask = LR == 64 ? ~0u : (1u << (LR % 32)) - 1;
-    const uint32_t starts = (uint32_t)(__ballot(is && q.start[at] >= 0) >> strip) & mask;
-    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end)) >> strip) & mask;
+    const uint32_t starts = (uint32_t)(__ballot(is && q.start[mine] >= 0) >> strip) & mask;
+    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[mine + 1] >= 0 || t0 + mine + 1 == t_end)) >> strip) & mask;
     auto initial = [&](int n, float *h) {
         int64_t from = (int64_t)n * p.D + ln.c;
         bool has = p.initial != nullptr && ln.live;
@@ -480,21 +487,18 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
         }
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            float av, uv;
-            token(s, e, av, uv);
-            b[e] = fmaf(av, b[e], uv);
-            A[e] *= av;
+            b[e] = fmaf(a[s][e], b[e], taken(s, e));
+            A[e] *= a[s][e];
         }
     }
     carry_in<VC, W, R>(x, hand, lane, w, tile, tiles, q.first_token < t0, q.first_token / TT, starts != 0, A, b, h);
     if constexpr (RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            forget(gr[s]);
-            if constexpr (sizeof(E) == 2) forget(xr[s]);
+            forget(xr[s]);
             if (BETA) forget(br[s]);
         }
-    E *y = (E *)p.y + (int64_t)tw * p.D + ln.c;
+    const int stored = ln.live ? nv : 0;               // tokens that this lane stores
     int seq = ends ? sequence_before<R>(q, w * S, lane) : 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -512,12 +516,10 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
         typename RE::T o = RE::zero();
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            float av, uv;
-            token(s, e, av, uv);
-            h[e] = fmaf(av, h[e], uv);
+            h[e] = fmaf(a[s][e], h[e], taken(s, e));
             RE::set(o, e, h[e]);
         }
-        if (s < nv && ln.live) RE::template store<STREAM>(y + (int64_t)s * p.D, o);
+        if (s < stored) RE::template store<STREAM>(at<E>(p.y, tw + s, p.D, ln.c), o);
         if ((ends >> s & 1) && p.final_state && ln.live) {
             int64_t to = (int64_t)seq * p.D + ln.c;
             bool kept = true;
@@ -535,23 +537,21 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
 // those of a lane lie in two groups where vectors overlap (two, see lane_of).
 template <typename E, int VC, bool HELD, bool STREAM> struct Saved {
     typename Vector<E, VC>::T r;
-    __device__ __forceinline__ void clear() { r = Vector<E, VC>::zero(); }
-    __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int, int c, bool) {
-        r = Vector<E, VC>::template load<STREAM>((const E *)v + row * stride + c);
+    __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int, uint32_t c, bool) {
+        r = Vector<E, VC>::template load<STREAM>(at<E>(v, row, stride, c));
     }
-    __device__ __forceinline__ float get(int e, int, bool) const { return Vector<E, VC>::get(r, e); }
+    __device__ __forceinline__ float get(int e, uint32_t, bool) const { return Vector<E, VC>::get(r, e); }
 };
 template <typename E, int VC, bool STREAM> struct Saved<E, VC, true, STREAM> {
     uint32_t codes, scales;                            // scales: of the first value's group low, of the last one's high
-    __device__ __forceinline__ void clear() { codes = scales = 0; }
-    __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, int c, bool two) {
-        const uint8_t *src = (const uint8_t *)h.codes + row * D + c;
-        const uint16_t *sc = (const uint16_t *)h.scales + row * ((D + kGroup - 1) / kGroup);
+    __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, uint32_t c, bool two) {
+        const uint8_t *src = at<uint8_t>(h.codes, row, D, c);
+        const int groups = (D + kGroup - 1) / kGroup;
         codes = VC == 4 ? *(const u32u *)src : VC == 2 ? *(const u16u *)src : *src;
-        scales = sc[c / kGroup];
-        if (two) scales |= (uint32_t)sc[(c + VC - 1) / kGroup] << 16;
+        scales = *at<uint16_t>(h.scales, row, groups, c / kGroup);
+        if (two) scales |= (uint32_t)*at<uint16_t>(h.scales, row, groups, (c + VC - 1) / kGroup) << 16;
     }
-    __device__ __forceinline__ float get(int e, int c, bool two) const {
+    __device__ __forceinline__ float get(int e, uint32_t c, bool two) const {
         const uint32_t s = two && (c + e) / kGroup != c / kGroup ? scales & 0xffff0000u : scales << 16;
         return held_byte(codes, e) * __uint_as_float(s);
     }
@@ -588,18 +588,20 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     typename RE::T dr[S];
     typename RG::T gr[S], br[S];
     float a[RAW ? 1 : S][VC];
-    const E *dp = (const E *)p.dy + (int64_t)tw * p.D;
-    const G *gp = (const G *)p.g + (int64_t)tw * p.g_stride, *bp = (const G *)p.beta + (int64_t)tw * p.beta_stride;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        dr[s] = RE::zero();
-        gr[s] = RG::zero();
-        if (s < nv && ln.live) {
-            dr[s] = RE::template load<STREAM>(dp + (int64_t)s * p.D + ln.c);
-            gr[s] = RG::template load<STREAM>(gp + s * p.g_stride + ln.c);
-        }
+    for (int s = 0; s < S; ++s) {                      // see scan_kernel
+        const int row = min(tw + s, t_end - 1);
+        dr[s] = RE::template load<STREAM>(at<E>(p.dy, row, p.D, ln.c));
+        gr[s] = RG::template load<STREAM>(at<G>(p.g, row, p.g_stride, ln.c));
     }
     find_sequences<TT, NT>(q, p, t0, t_end);
+    if (nv < S)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (s >= nv) {
+                dr[s] = RE::zero();
+                gr[s] = RG::zero();
+            }
     if constexpr (!RAW)
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -615,25 +617,19 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     SV yr[S], xr[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        yr[s].clear();
+        const int row = min(tw + s, t_end - 1);
+        yr[s].load(p.y, p.y8, max(row - 1, 0), p.D, p.D, ln.c, two);
         if (BETA) {
-            xr[s].clear();
-            br[s] = RG::zero();
-        }
-        if (s < nv && ln.live) {
-            yr[s].load(p.y, p.y8, max(tw + s - 1, 0), p.D, p.D, ln.c, two);
-            if (BETA) {
-                xr[s].load(p.x, p.x8, tw + s, p.x_stride, p.D, ln.c, two);
-                br[s] = RG::template load<STREAM>(bp + s * p.beta_stride + ln.c);
-            }
+            xr[s].load(p.x, p.x8, row, p.x_stride, p.D, ln.c, two);
+            br[s] = RG::template load<STREAM>(at<G>(p.beta, row, p.beta_stride, ln.c));
         }
     }
     const bool is = lane < nv;
-    const int at = w * S + min(lane, S - 1);
+    const int mine = w * S + min(lane, S - 1);
     const int strip = threadIdx.x % 64 / LR * LR;      // its first lane
     const uint32_t mask = LR == 64 ? ~0u : (1u << (LR % 32)) - 1;
-    const uint32_t starts = (uint32_t)(__ballot(is && q.start[at] >= 0) >> strip) & mask;
-    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[at + 1] >= 0 || t0 + at + 1 == t_end)) >> strip) & mask;
+    const uint32_t starts = (uint32_t)(__ballot(is && q.start[mine] >= 0) >> strip) & mask;
+    const uint32_t ends = (uint32_t)(__ballot(is && (q.start[mine + 1] >= 0 || t0 + mine + 1 == t_end)) >> strip) & mask;
     const int seq = ends ? sequence_before<R>(q, w * S, lane) : 0;   // of the wave's first token, unless one begins with it
     // the gradient of the final state of the sequence that ends with token s
     auto final_gradient = [&](int s, float *c) {
@@ -670,7 +666,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
             forget(gr[s]);
             forget(dr[s]);
         }
-    const int64_t out = (int64_t)tw * p.D + ln.c;
+    const int stored = ln.live ? nv : 0;               // tokens that this lane stores
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
         const bool first = starts >> s & 1;
@@ -697,10 +693,10 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
                 RE::set(ox, e, dh);
             }
         }
-        if (s < nv && ln.live) {
-            RE::template store<STREAM>((E *)p.dx + out + (int64_t)s * p.D, ox);
-            RG::template store<STREAM>((G *)p.dg + out + (int64_t)s * p.D, og);
-            if (BETA) RG::template store<STREAM>((G *)p.dbeta + out + (int64_t)s * p.D, ob);
+        if (s < stored) {
+            RE::template store<STREAM>(at<E>(p.dx, tw + s, p.D, ln.c), ox);
+            RG::template store<STREAM>(at<G>(p.dg, tw + s, p.D, ln.c), og);
+            if (BETA) RG::template store<STREAM>(at<G>(p.dbeta, tw + s, p.D, ln.c), ob);
         }
         if (first && p.dinitial && ln.live) store_states<VC>(p.dinitial, (int64_t)n * p.D + ln.c, 0, c);
     }
@@ -780,10 +776,16 @@ struct Tile {
 // By the number of channels: one a lane below 4, four strips a wave up to 64.
 enum Width { kOne, kNarrow, kWide };
 Width width_of(int D) { return D < 4 ? kOne : D <= 64 ? kNarrow : kWide; }
-constexpr Tile tile_of(Width width, bool gate_f32, bool backward, bool beta, bool held) {
-    if (width != kWide) return {width == kOne ? 1 : 4, 8, backward && gate_f32 ? 4 : 8, 4};
-    if (backward) return gate_f32 ? Tile{4, 8, 4, 1} : beta && !held ? Tile{2, 8, 16, 1} : Tile{4, 8, 8, 1};
-    return gate_f32 ? Tile{4, 8, 8, 1} : Tile{2, 8, 16, 1};
+// What a call's tensors are, as far as its tiles go by it.
+struct Kind {
+    bool backward, f32, gate_f32, beta, held;
+};
+constexpr Tile tile_of(Width width, Kind k) {
+    if (width != kWide) return {width == kOne ? 1 : 4, 8, k.backward && k.gate_f32 ? 4 : 8, 4};
+    if (!k.backward)
+        return k.gate_f32 ? (k.beta ? Tile{4, 8, 8, 1} : Tile{2, 8, 20, 1}) : Tile{2, 8, k.beta ? 20 : 28, 1};
+    if (k.gate_f32) return k.held ? Tile{4, 8, 4, 1} : Tile{2, 8, k.f32 ? 8 : 10, 1};
+    return !k.beta ? Tile{4, 8, 10, 1} : k.held ? Tile{4, 8, 6, 1} : Tile{2, 8, 14, 1};
 }
 int tiles_of(int64_t T_tot, const Tile &t) { return (int)std::max<int64_t>((T_tot + t.tokens() - 1) / t.tokens(), 1); }
 int blocks_of(int D, const Tile &t) { return t.R > 1 ? 1 : t.VC == 2 ? column_blocks<2>(D) : column_blocks<4>(D); }
@@ -796,7 +798,8 @@ template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
     return (int64_t)p.T_tot * p.D * token > 256 << 20;
 }
 template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
-    constexpr Tile f = tile_of(WIDTH, sizeof(G) == 4, false, BETA, HELD), b = tile_of(WIDTH, sizeof(G) == 4, true, BETA, HELD);
+    constexpr Tile f = tile_of(WIDTH, {false, sizeof(E) == 4, sizeof(G) == 4, BETA, HELD});
+    constexpr Tile b = tile_of(WIDTH, {true, sizeof(E) == 4, sizeof(G) == 4, BETA, HELD});
     constexpr bool wide = WIDTH == kWide;
     const Tile t = pass == kForward ? f : b;
     const int tiles = tiles_of(p.T_tot, t), ncb = blocks_of(p.D, t);
@@ -854,7 +857,7 @@ hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, h
 
 // Over the tiles that calls of these sizes and types take: f(tile).
 template <typename F> void each_tile(int D, int gate_f32, bool backward, F f) {
-    for (int i = 0; i < 4; ++i) f(tile_of(width_of(D), gate_f32 != 0, backward, i & 1, i & 2));
+    for (int i = 0; i < 8; ++i) f(tile_of(width_of(D), {backward, gate_f32 && (i & 4), gate_f32 != 0, (i & 1) != 0, (i & 2) != 0}));
 }
 size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward) {
     size_t most = 0;
