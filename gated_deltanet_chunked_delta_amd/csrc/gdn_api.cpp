@@ -473,6 +473,7 @@ int check_norm_ws(const gdn_norm_shape &s, const float *dweight, const void *wor
 }
 
 // Sizes of a gated linear recurrence.
+constexpr int64_t kMaxScanTokens = INT_MAX - 1024;     // a tile behind the last token has a number of 32 bits too
 int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with_beta) {
     if (!shape) return GDN_ERR_NULL;
     const gdn_scan_shape &s = *shape;
@@ -481,7 +482,7 @@ int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with
     if (s.gate_dtype != s.dtype && s.gate_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
     if (cu_seqlens ? s.B != 1 : s.N != s.B) return GDN_ERR_SHAPE;
     const int64_t tokens = (int64_t)s.B * s.T, most = (int64_t)1 << 31;
-    if (tokens > INT_MAX - 64 || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
+    if (tokens > kMaxScanTokens || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
     if (tokens > 0 && (s.x_stride < s.D || s.g_stride < s.D || (with_beta && s.beta_stride < s.D))) return GDN_ERR_SHAPE;
     if (s.x_stride > most || s.g_stride > most || (with_beta && s.beta_stride > most)) return GDN_ERR_SHAPE;
     if (gdn::scan_grid(tokens, s.D, s.N) > kMaxGrid) return GDN_ERR_SHAPE;
@@ -929,7 +930,7 @@ size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward) {
     if (!shape || shape->B < 0 || shape->T < 0 || shape->D <= 0 || shape->D > (1 << 26)) return 0;
     if (gdn::elem_bytes(shape->dtype) == 0 || gdn::elem_bytes(shape->gate_dtype) == 0) return 0;
     const int64_t tokens = (int64_t)shape->B * shape->T;
-    if (tokens > INT_MAX - 64) return 0;
+    if (tokens > kMaxScanTokens) return 0;
     return gdn::scan_workspace_bytes(tokens, shape->D, scan_gate_f32(*shape), backward != 0);
 }
 

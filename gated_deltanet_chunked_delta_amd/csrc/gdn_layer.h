@@ -11,8 +11,8 @@ namespace gdn {
 
 // Kernel kinds of the timing hook, after those of gdn_internal.h.
 enum LayerKernelKind { kStepsKernel = kNumKernelKinds, kConvKernel, kConvUpdateKernel, kConvBwdKernel, kNormKernel,
-                       kNormBwdKernel, kColumnSumKernel, kScanKernel, kScanStepsKernel, kScanBwdKernel,
-                       kQuantKernel, kDequantKernel, kNumAllKinds };
+                       kNormBwdKernel, kColumnSumKernel, kScanClearKernel, kScanKernel, kScanStepsKernel,
+                       kScanBwdKernel, kQuantKernel, kDequantKernel, kNumAllKinds };
 const char *layer_kernel_name(int kind);
 
 // Slots of a pool that a few-token step reads and writes: sequence n starts
@@ -116,7 +116,7 @@ struct QuantParams {
     int value_rows, held_rows;
 };
 hipError_t launch_quant(const QuantParams &p, int dtype, int bits, bool back, hipStream_t stream, Profiler *prof);
-int64_t quant_grid(int64_t n, int64_t D);
+int64_t quant_grid(int64_t n, int64_t D);   // as for scan_grid
 
 // The gated linear recurrence h_t = e^g_t h_(t-1) + beta_t x_t per channel.
 struct ScanParams {
@@ -140,6 +140,8 @@ struct ScanParams {
 };
 // gate_f32: g, beta and their gradients are fp32 (else the element type).
 size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward);
+// 256-thread workgroups of the largest grid these sizes launch (host check against the
+// grid limit).
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N);
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
 hipError_t launch_scan_bwd(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);

@@ -371,6 +371,7 @@ const char *layer_kernel_name(int kind) {
         case kNormKernel: return "norm_kernel";
         case kNormBwdKernel: return "norm_bwd_kernel";
         case kColumnSumKernel: return "column_sum_kernel";
+        case kScanClearKernel: return "scan_clear_kernel";
         case kScanKernel: return "scan_kernel";
         case kScanStepsKernel: return "scan_steps_kernel";
         case kScanBwdKernel: return "scan_bwd_kernel";

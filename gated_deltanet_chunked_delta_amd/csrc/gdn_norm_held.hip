@@ -7,6 +7,10 @@
 // Bound by HBM.  Against the norm that keeps x and z as they are the forward pass
 // writes two bytes more an element (bf16: 8.1 instead of 6) and the backward pass
 // reads two less (8.1 instead of 10); what lives from one to the other is halved.
+// 524,288 rows of 128 in bf16 take 100 us forward (5.5 TB/s) and 117 us backward (4.7
+// TB/s, 5 more for the sums of dweight); the backward pass does 36 instructions an
+// element, two thirds of its time.  Rows that are not of whole eights load and store
+// their last elements by fours, twos and one: 32,752 rows of 100 backward 13 us.
 #include <algorithm>
 
 #include "gdn_norm_device.h"
@@ -93,7 +97,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
 }
 
 // Workgroups of 512 threads: twice the waves of the norm's backward pass for as many
-// rows of partial sums, as there is more arithmetic for fewer bytes.
+// rows of partial sums, as there is more arithmetic for fewer bytes (524,288 rows of
+// 128: 117 us; with 256 threads, the next row's loads the only ones in flight, 174; with
+// 1024 119).
 constexpr int kBwdThreads = 512;
 template <typename E, int L, int NV, bool STREAM>
 __global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 4 : 2) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {

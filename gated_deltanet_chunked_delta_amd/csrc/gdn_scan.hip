@@ -4,6 +4,24 @@
 //   dh_t = dy_t + e^(g_(t+1)) dh_(t+1)     (dht added at a sequence's last token)
 //   dx = beta dh,  dbeta = x dh,  dg_t = e^(g_t) h_(t-1) dh_t,  dh0 = e^(g_1) dh_1
 // with h_(t-1) the forward's y_(t-1) as it was rounded, or the initial state.
+//
+// Bound by HBM where there are tokens enough: each input is read once and each output
+// written once.  The recurrence is serial in the tokens, but what a run of tokens does
+// to a state is a map h -> A h + b, and maps compose: workgroups take tiles of tokens
+// and channels, keep them in registers, hand their maps on to the later ones (see
+// carry_in) and run through their tokens again with the state that comes in, so that
+// nothing is read twice.  A pass over the data for the maps and another for the
+// outputs would read x and the gates twice.
+//
+// Measured (GPU time): 131,072 tokens of 4096 channels with bf16 gates and no beta 643
+// us (5.0 TB/s of x, g and y; one thread a channel 106 ms); 64 packed prompts, 74,000
+// tokens of 4096, fp32 g and beta 636 us (5.7 TB/s; 2.66 ms); gradients of 16,384
+// tokens of 4096 with fp32 gates 276 us (5.8 TB/s; 5.7 ms), of the packed prompts with
+// bf16 gates and x and y in 8 bits 893 us (4.8 TB/s; 3.3 ms).  Few tokens or channels
+// are bound by the latency of a tile, about 15 us: loads 3, decays and sums 3, maps
+// of other tiles 4, stores 2 (2042 tokens of 1001 channels in fp32 15 us, and 2 for
+// the workspace); long sequences of few channels by the states' way from block to
+// block (131,072 tokens of 256 channels 125 us, floor 84; 2^20 of 64 192, floor 84).
 #include <algorithm>
 #include <type_traits>
 
@@ -20,12 +38,12 @@ namespace {
 using namespace dev;
 
 // e^g for g <= 0, with a relative error of at most 0.62 2^-24 down to -0.1, 1.3 2^-24
-// to -5 and 5.1 2^-24 to -87, and 0 below: n = the integer
-// nearest to g / ln 2, r = g - n ln 2, e^r = 1 + r + r^2 p(r) with p of degree 4
-// interpolating at Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n added to the
-// exponent.  The sum g / ln 2 + 1.5 2^23 has n in its low bits.  11 instructions; the
-// hardware exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on
-// average, which a channel sums over all the tokens that it remembers.
+// to -5 and 5.1 2^-24 to -87, and 0 below: n = the integer nearest to g / ln 2,
+// r = g - n ln 2, e^r = 1 + r + r^2 p(r) with p of degree 4 interpolating at
+// Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n added to the exponent.  The sum
+// g / ln 2 + 1.5 2^23 has n in its low bits.  11 instructions; the hardware
+// exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on average,
+// which a channel sums over all the tokens that it remembers (it would save 1 to 5 %).
 __device__ __forceinline__ float decay(float g) {
     const float t = fmaf(g, 1.4426950408889634f, kRoundBias);
     const float r = fmaf(t - kRoundBias, -0.6931471805599453f, g);
@@ -69,7 +87,8 @@ template <typename E> struct Vector<E, 1> {
 };
 
 // A value that the compiler takes to be another one, so that what was computed from it
-// is computed again instead of being kept.
+// is computed again instead of being kept: two widened bf16 values take two registers,
+// the pair as loaded one.
 template <typename T> __device__ __forceinline__ void forget(T &r) {
     typedef std::conditional_t<sizeof(T) == 8, unsigned long long, std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>> U;
     U v = __builtin_bit_cast(U, r);
@@ -179,7 +198,8 @@ template <int VC, int LR> __device__ __forceinline__ void await(const unsigned l
         to[e][0] = float2{__uint_as_float((uint32_t)(v[e] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v[e])};
 }
 
-__global__ void __launch_bounds__(256) clear_kernel(uint4 *w, int64_t n) {
+// The words' flags, before any tile sets one, and the counter.
+__global__ void __launch_bounds__(256) scan_clear_kernel(uint4 *w, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) w[i] = uint4{0, 0, 0, 0};
 }
 
@@ -705,6 +725,9 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
 // A few tokens per sequence, states in a pool: see StepSlots.  A wave takes the
 // channels of a column block of one sequence; kAhead tokens are loaded before the
 // first of them is used, as the wave's own stores are in the way of later loads.
+// Bound by the launch and two trips to memory, slots then states: one sequence of four
+// tokens of 4096 channels 5.2 us, 64 of them with a slot a token 7.8 us (a call from
+// Python takes 10).
 constexpr int kAhead = 4;
 template <typename E, typename G, bool BETA, int VC> __global__ void __launch_bounds__(64) scan_steps_kernel(ScanParams p, int ncb) {
     typedef Vector<E, VC> RE;
@@ -766,14 +789,25 @@ template <typename E, typename G, bool BETA> void launch_steps_vc(const ScanPara
 }
 
 enum Pass { kForward, kBackward, kSteps };
-// Channels of a lane, waves of a workgroup, tokens of a strip and strips of a wave, for
-// at least two workgroups a CU (128 registers a lane) and few tiles to hand states
-// through.
+// Channels of a lane, waves of a workgroup, tokens of a strip and strips of a wave: as
+// many tokens as two workgroups a CU have registers for (128 a lane), so that one
+// loads while the other waits or computes, and as few tiles as that gives to hand
+// states through.  Measured beside their neighbours:
+//   131,072 x 4096, bf16 gates, no beta: 28 tokens 643 us, 24 663, 32 694 (spilled), 16
+//     737, four channels by 12 tokens 701, by 8 788
+//   with beta: 20 tokens 801, 16 831, four channels by 8 893
+//   packed prompts, fp32 g and beta: four channels by 8 tokens 644, by 9 659, by 7 660, two
+//     by 16 (one workgroup a CU) 904
+//   backward, fp32 gates: two channels by 10 tokens 280, by 8 336, four by 4 290; fp32
+//     tensors two by 8 374, by 10 413; held four by 4 276, two by 10 425
+//   backward, bf16 gates: two channels by 14 tokens 732, four by 8 758; held four by 6
+//     896, by 5 962, by 7 959; without beta four by 10 265, by 8 274, two by 16 270
 struct Tile {
     int VC, W, S, R;
     constexpr int tokens() const { return W * R * S; }
 };
-// By the number of channels: one a lane below 4, four strips a wave up to 64.
+// By the number of channels: one a lane below 4, four strips a wave up to 64 (2^20
+// tokens of 8 channels with one strip a wave: 715 against 200 us, of 64 274 against 192).
 enum Width { kOne, kNarrow, kWide };
 Width width_of(int D) { return D < 4 ? kOne : D <= 64 ? kNarrow : kWide; }
 // What a call's tensors are, as far as its tiles go by it.
@@ -781,7 +815,7 @@ struct Kind {
     bool backward, f32, gate_f32, beta, held;
 };
 constexpr Tile tile_of(Width width, Kind k) {
-    if (width != kWide) return {width == kOne ? 1 : 4, 8, k.backward && k.gate_f32 ? 4 : 8, 4};
+    if (width != kWide) return {width == kOne ? 1 : 4, 8, k.backward ? (k.gate_f32 ? 4 : 5) : k.gate_f32 ? 8 : 10, 4};
     if (!k.backward)
         return k.gate_f32 ? (k.beta ? Tile{4, 8, 8, 1} : Tile{2, 8, 20, 1}) : Tile{2, 8, k.beta ? 20 : 28, 1};
     if (k.gate_f32) return k.held ? Tile{4, 8, 4, 1} : Tile{2, 8, k.f32 ? 8 : 10, 1};
@@ -791,13 +825,15 @@ int tiles_of(int64_t T_tot, const Tile &t) { return (int)std::max<int64_t>((T_to
 int blocks_of(int D, const Tile &t) { return t.R > 1 ? 1 : t.VC == 2 ? column_blocks<2>(D) : column_blocks<4>(D); }
 int64_t row_words(int D, const Tile &t) { return (int64_t)blocks_of(D, t) * t.VC * (64 / t.R); }
 
-// Passes over more than the 256 MiB of the last cache are streamed past it.
+// Passes over more than the 256 MiB of the last cache are streamed past it: packed
+// prompts 645 against 699 us, gradients of 16,384 tokens 286 against 311; smaller ones
+// lose by it (2042 tokens of 1001 channels 22.4 against 21.2 us).
 template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
     const int gates = p.beta ? 2 : 1, kept = p.y8.codes ? gates : gates * (int)sizeof(E);
     const int token = pass == kForward ? 2 * sizeof(E) + gates * sizeof(G) : 2 * sizeof(E) + 2 * gates * sizeof(G) + kept;
     return (int64_t)p.T_tot * p.D * token > 256 << 20;
 }
-template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st) {
+template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st, Profiler *prof) {
     constexpr Tile f = tile_of(WIDTH, {false, sizeof(E) == 4, sizeof(G) == 4, BETA, HELD});
     constexpr Tile b = tile_of(WIDTH, {true, sizeof(E) == 4, sizeof(G) == 4, BETA, HELD});
     constexpr bool wide = WIDTH == kWide;
@@ -805,8 +841,12 @@ template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch
     const int tiles = tiles_of(p.T_tot, t), ncb = blocks_of(p.D, t);
     if (tiles > 1) {
         const int64_t n = handed_words(tiles, row_words(p.D, t)) / 2;
-        clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>((uint4 *)p.ws, n);
+        if (prof) prof->begin(kScanClearKernel, st);
+        scan_clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>((uint4 *)p.ws, n);
+        if (prof) prof->end(kScanClearKernel, st);
     }
+    const int kind = pass == kForward ? kScanKernel : kScanBwdKernel;
+    if (prof) prof->begin(kind, st);
     const unsigned grid = (unsigned)(tiles * ncb);
     const bool stream = wide && streams<E, G>(p, pass);
     if (pass == kBackward) {
@@ -820,37 +860,36 @@ template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch
         else
             scan_kernel<E, G, BETA, false, f.VC, f.W, f.S, f.R><<<grid, f.W * 64, 0, st>>>(p, ncb, tiles);
     }
+    if (prof) prof->end(kind, st);
 }
-template <typename E, typename G, bool BETA, bool HELD> void launch_width(const ScanParams &p, Pass pass, hipStream_t st) {
+template <typename E, typename G, bool BETA, bool HELD> void launch_width(const ScanParams &p, Pass pass, hipStream_t st, Profiler *prof) {
     switch (width_of(p.D)) {
-        case kOne: return launch_tiles<E, G, BETA, HELD, kOne>(p, pass, st);
-        case kNarrow: return launch_tiles<E, G, BETA, HELD, kNarrow>(p, pass, st);
-        case kWide: return launch_tiles<E, G, BETA, HELD, kWide>(p, pass, st);
+        case kOne: return launch_tiles<E, G, BETA, HELD, kOne>(p, pass, st, prof);
+        case kNarrow: return launch_tiles<E, G, BETA, HELD, kNarrow>(p, pass, st, prof);
+        case kWide: return launch_tiles<E, G, BETA, HELD, kWide>(p, pass, st, prof);
     }
 }
-template <typename E, typename G, bool HELD> void launch_beta(const ScanParams &p, Pass pass, hipStream_t st) {
-    p.beta ? launch_width<E, G, true, HELD>(p, pass, st) : launch_width<E, G, false, HELD>(p, pass, st);
+template <typename E, typename G, bool HELD> void launch_beta(const ScanParams &p, Pass pass, hipStream_t st, Profiler *prof) {
+    p.beta ? launch_width<E, G, true, HELD>(p, pass, st, prof) : launch_width<E, G, false, HELD>(p, pass, st, prof);
 }
-template <typename E, typename G> void launch_e(const ScanParams &p, Pass pass, hipStream_t st) {
+template <typename E, typename G> void launch_e(const ScanParams &p, Pass pass, hipStream_t st, Profiler *prof) {
     if (pass != kSteps) {
-        p.y8.codes ? launch_beta<E, G, true>(p, pass, st) : launch_beta<E, G, false>(p, pass, st);
+        p.y8.codes ? launch_beta<E, G, true>(p, pass, st, prof) : launch_beta<E, G, false>(p, pass, st, prof);
         return;
     }
+    if (prof) prof->begin(kScanStepsKernel, st);
     p.beta ? launch_steps_vc<E, G, true>(p, st) : launch_steps_vc<E, G, false>(p, st);
+    if (prof) prof->end(kScanStepsKernel, st);
 }
 hipError_t launch_any(const ScanParams &p, Pass pass, int dtype, int gate_f32, hipStream_t st, Profiler *prof) {
     if (p.N == 0) return hipSuccess;
-    const int kind = pass == kForward ? kScanKernel : pass == kBackward ? kScanBwdKernel : kScanStepsKernel;
-    if (prof) prof->begin(kind, st);
     if (dtype != 0)
-        launch_e<float, float>(p, pass, st);
+        launch_e<float, float>(p, pass, st, prof);
     else if (gate_f32)
-        launch_e<bf16, float>(p, pass, st);
+        launch_e<bf16, float>(p, pass, st, prof);
     else
-        launch_e<bf16, bf16>(p, pass, st);
-    const hipError_t err = hipGetLastError();
-    if (prof) prof->end(kind, st);
-    return err;
+        launch_e<bf16, bf16>(p, pass, st, prof);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -870,7 +909,9 @@ size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward) {
 int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N) {
     int64_t most = N * steps_blocks((int)D);
     for (int i = 0; i < 4; ++i)
-        each_tile((int)D, i & 1, i & 2, [&](const Tile &t) { most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t)); });
+        each_tile((int)D, i & 1, i & 2, [&](const Tile &t) {
+            most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t) * (t.W * 64 / 256));
+        });
     return most;
 }
 

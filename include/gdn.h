@@ -684,7 +684,7 @@ size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward);
  * workspace.  Tensors are aligned to their element.  Arithmetic is fp32, out
  * rounded once, and the result of a call does not depend on scheduling.  Returns
  * GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a sequence, more than
- * 2^31 - 65 of them, or too many for one launch), GDN_ERR_DTYPE,
+ * 2^31 - 1025 of them, or too many for one launch: 2^23 - 1 tiles), GDN_ERR_DTYPE,
  * GDN_ERR_UNSUPPORTED (gate_dtype), GDN_ERR_ALIGN, GDN_ERR_WORKSPACE or
  * GDN_ERR_LAUNCH. */
 int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state,
