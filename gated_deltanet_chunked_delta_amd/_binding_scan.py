@@ -347,6 +347,8 @@ def _held_rows(c, rows, D, dev, name):
         raise ValueError(f"{name}: a checkpoint has int8 codes and bfloat16 scales")
     if codes.numel() != rows * D or scales.numel() != rows * -(-D // GROUP):
         raise ValueError(f"{name}: codes and scales must be those of {rows} rows of {D} values")
+    if codes.dim() == 0 or (codes.shape[-1] != D and (D % GROUP or codes.shape[-1] % GROUP)):
+        raise ValueError(f"{name}: a checkpoint of other rows than {D} values needs both in whole groups of {GROUP}")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}")
     codes, scales = codes.contiguous(), scales.contiguous()

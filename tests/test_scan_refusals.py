@@ -84,6 +84,11 @@ REFUSED = {
     "gradient of a tensor and a checkpoint": lambda: _bwd(x=_ck()),
     "gradient of codes of other values": lambda: _bwd(x=_ck((2, 4, 9)), y=_ck()),
     "gradient of scales of other groups": lambda: _bwd(x=_ck(), y=_ck(groups=2)),
+    # as many scales as rows of 62 have, but of groups that end with each 31 values
+    "gradient of codes of two heads of 31": lambda: _bwd(x=(1, 4, 62), dy=(1, 4, 62), beta=None, y=_ck((1, 4, 2, 31))),
+    "gradient of codes of longer rows": lambda: _bwd(x=(1, 2, 31), dy=(1, 2, 31), beta=None, y=_ck((1, 62), 2)),
+    "norm gradient of codes of two heads of 31": lambda: gdn.fused_gated_rms_norm_checkpoint_bwd(
+        _ck((3, 2, 31)), _ck((3, 62), 2), Z(62), Z(3, 62)),
     "gradient of uint8 codes": lambda: _bwd(x=_ck(cdt=U8), y=_ck()),
     "gradient of fp32 scales": lambda: _bwd(x=_ck(), y=_ck(sdt=F32)),
     "gradient dht of another shape": lambda: _bwd(dht=Z(2, 9)),
