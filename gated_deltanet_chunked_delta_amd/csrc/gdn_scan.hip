@@ -13,15 +13,15 @@
 // nothing is read twice.  A pass over the data for the maps and another for the
 // outputs would read x and the gates twice.
 //
-// Measured (GPU time): 131,072 tokens of 4096 channels with bf16 gates and no beta 643
-// us (5.0 TB/s of x, g and y; one thread a channel 106 ms); 64 packed prompts, 74,000
+// Measured (GPU time): 131,072 tokens of 4096 channels with bf16 gates and no beta 650
+// us (4.9 TB/s of x, g and y; one thread a channel 106 ms); 64 packed prompts, 74,000
 // tokens of 4096, fp32 g and beta 636 us (5.7 TB/s; 2.66 ms); gradients of 16,384
 // tokens of 4096 with fp32 gates 276 us (5.8 TB/s; 5.7 ms), of the packed prompts with
 // bf16 gates and x and y in 8 bits 893 us (4.8 TB/s; 3.3 ms).  Few tokens or channels
 // are bound by the latency of a tile, about 15 us: loads 3, decays and sums 3, maps
 // of other tiles 4, stores 2 (2042 tokens of 1001 channels in fp32 15 us, and 2 for
 // the workspace); long sequences of few channels by the states' way from block to
-// block (131,072 tokens of 256 channels 125 us, floor 84; 2^20 of 64 192, floor 84).
+// block (131,072 tokens of 256 channels 126 us, floor 84; 2^20 of 64 197, floor 84).
 #include <algorithm>
 #include <type_traits>
 
@@ -176,23 +176,32 @@ template <int VC, int LR> __device__ __forceinline__ Handed handed_of(void *ws, 
 
 // A word carries its own flag, the sign of its upper half (decays are not negative),
 // so that it is handed on without a fence: one 64-bit store and loads that repeat
-// until the flag is there, past the caches that are not shared.
+// until the flag is there, past the caches that are not shared.  The wait is bounded:
+// only where another call writes the same workspace meanwhile does a word fail to come,
+// and then, after some seconds, NaNs are taken for it.
+constexpr int kMaxPolls = 1 << 22;
 __device__ __forceinline__ void put(unsigned long long *w, float A, float h) {
     __hip_atomic_store(w, (unsigned long long)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(h),
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <int VC, int LR> __device__ __forceinline__ void await(const unsigned long long *w, float2 (*to)[LR]) {
     unsigned long long v[VC];
-    for (;;) {
+    int polls = 0;
+    for (;;) {                                         // the wave's lanes wait together
         bool all = true;
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
             v[e] = __hip_atomic_load(w + e * LR, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             all = all && (long long)v[e] < 0;
         }
-        if (all) break;
+        if (__ballot(!all) == 0 || polls == kMaxPolls) break;
+        ++polls;
         __builtin_amdgcn_s_sleep(1);
     }
+    if (polls == kMaxPolls)
+#pragma unroll
+        for (int e = 0; e < VC; ++e)
+            if ((long long)v[e] >= 0) v[e] = 0x7fc000007fc00000ull;
 #pragma unroll
     for (int e = 0; e < VC; ++e)
         to[e][0] = float2{__uint_as_float((uint32_t)(v[e] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v[e])};
@@ -287,7 +296,8 @@ template <int R, int TT> __device__ __forceinline__ int sequence_before(const Se
 
 // Tiles are taken in the order of a counter, so that whatever tile a workgroup waits
 // for is with a workgroup that runs already; as each hands its map on before it
-// waits, and the earliest one waits for none, every wait ends.
+// waits, and the earliest one waits for none, every wait ends.  A number past the last
+// tile's, which only a workspace that another call uses meanwhile can give, is none's.
 __device__ __forceinline__ int next_tile(void *ws, int tiles, int *ticket) {
     if (tiles == 1) return blockIdx.x;
     if (threadIdx.x == 0) *ticket = (int)atomicAdd((uint32_t *)ws, 1u);
@@ -423,6 +433,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
     __shared__ int ticket;
     const int lane = threadIdx.x % LR, w = strip_int<R>(threadIdx.x / LR);   // in the strip; the strip
     const int id = next_tile(p.ws, tiles, &ticket);
+    if ((uint32_t)id >= (uint32_t)(tiles * ncb)) return;
     const Handed hand = handed_of<VC, LR>(p.ws, tiles, ncb, id % ncb, lane);
     const int tile = id / ncb, t0 = tile * TT;
     const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
@@ -586,6 +597,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     __shared__ int ticket;
     const int lane = threadIdx.x % LR, w = strip_int<R>(threadIdx.x / LR);   // in the strip; the strip
     const int id = next_tile(p.ws, tiles, &ticket);
+    if ((uint32_t)id >= (uint32_t)(tiles * ncb)) return;
     const Handed hand = handed_of<VC, LR>(p.ws, tiles, ncb, id % ncb, lane);
     const int place = id / ncb, tile = tiles - 1 - place, t0 = tile * TT;
     const Lane ln = lane_of<VC>(p.D, ncb, id % ncb, lane);
@@ -807,7 +819,7 @@ struct Tile {
     constexpr int tokens() const { return W * R * S; }
 };
 // By the number of channels: one a lane below 4, four strips a wave up to 64 (2^20
-// tokens of 8 channels with one strip a wave: 715 against 200 us, of 64 274 against 192).
+// tokens of 8 channels with one strip a wave: 715 against 204 us, of 64 274 against 197).
 enum Width { kOne, kNarrow, kWide };
 Width width_of(int D) { return D < 4 ? kOne : D <= 64 ? kNarrow : kWide; }
 // What a call's tensors are, as far as its tiles go by it.

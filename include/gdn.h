@@ -678,7 +678,8 @@ size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward);
  *   final_state   [N, D]      fp32 or NULL written (an empty sequence's is its
  *                 initial state); may alias initial_state exactly
  *   workspace     gdn_scan_workspace_bytes bytes, 16-byte aligned
- *                 (GDN_ERR_WORKSPACE); contents on entry are ignored
+ *                 (GDN_ERR_WORKSPACE); contents on entry are ignored; calls that may
+ *                 run at the same time need workspaces of their own
  *
  * Outputs must not overlap each other, the inputs (final_state aside) or the
  * workspace.  Tensors are aligned to their element.  Arithmetic is fp32, out
