@@ -198,9 +198,10 @@ def gated_linear_recurrence(x, g, beta=None, initial_state=None, output_final_st
     With ``state_pool`` [P,D] (float32 or bfloat16) and ``state_indices`` [N] int32,
     sequence n starts from slot state_indices[n] (from zeros if
     ``read_initial_state`` is False or the slot is outside the pool) and leaves
-    its final state there; the call then returns ``(y, None)``.  A preallocated
-    uint8 ``workspace`` of gdn_scan_workspace_bytes bytes or more, 16-byte
-    aligned, may be given.
+    its final state there (no slot may be named twice); the call then returns
+    ``(y, None)``.  A preallocated uint8 ``workspace`` of gdn_scan_workspace_bytes
+    bytes or more, 16-byte aligned, may be given; calls that may run at the same
+    time need their own.
     """
     dev, x, g, beta, cu, shape, N = _scan_args(x, g, beta, cu_seqlens)
     D = shape.D
@@ -282,7 +283,8 @@ def gated_linear_recurrence_bwd(x, g, y, dy, beta=None, dht=None, initial_state=
     only with ``beta`` (it may be None without).  y, and with beta x, may instead
     be the Checkpoints of these tensors (y's may come from
     fused_gated_rms_norm_checkpoint, with y seen as [B,T,heads,dim] and dim a
-    multiple of 32): the gradients are then taken at the values that they stand for.
+    multiple of 32; other dims are refused): the gradients are then taken at the
+    values that they stand for.
     Returns ``(dx, dg, dbeta, dinitial)``: dx in dy's dtype, dg and dbeta in the
     gates', dinitial [N,D] float32; dbeta is None without beta, dinitial None
     unless ``output_dinitial``.  ``workspace`` as for the forward call, of

@@ -694,7 +694,8 @@ int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *in
 
 /* gdn_scan_fwd with the states in a pool [pool_size, D], fp32 or bf16, in place, as
  * gdn_chunk_fwd_pool has them: a slot outside the pool gives a sequence a zero
- * start and stores nothing; read_initial = 0 starts all of them from zero. */
+ * start and stores nothing; read_initial = 0 starts all of them from zero.  Two
+ * sequences must not name the same slot. */
 int gdn_scan_fwd_pool(const void *x, const void *g, const void *beta, const gdn_state_pool *pool,
                       const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *workspace,
                       size_t workspace_bytes, void *stream);
@@ -710,8 +711,10 @@ int gdn_scan_steps(const void *x, const void *g, const void *beta, const gdn_ste
  * last one may be shorter).  With top = 127 (8 bits) or 7 (4 bits) a group's scale s
  * is the smallest bf16 number that has top * s >= the largest magnitude in it, and
  * 0 where that is below 2^-100; a value's code is the integer nearest to value / s,
- * ties to even, in [-top, top]; it stands for code * s.  A group that holds an
- * infinity or a NaN has a NaN scale and stands for NaNs.
+ * ties to even, in [-top, top]; it stands for code * s, which is rounded to the type
+ * it is restored to (magnitudes within half a code of the type's largest may so
+ * become infinities).  A group that holds an infinity or a NaN has a NaN scale and
+ * stands for NaNs.
  *
  *   codes         [rows, D] int8, or [rows, (D + 1) / 2] bytes with element 2i in
  *                 the low and 2i + 1 in the high half of byte i, two's complement
