@@ -23,6 +23,7 @@ EXPORTED_SCAN = ("gdn_scan_fwd", "gdn_scan_fwd_pool", "gdn_scan_steps", "gdn_sca
                  "gdn_hold", "gdn_restore", "gdn_gated_norm_hold", "gdn_gated_norm_hold_bwd")
 
 GROUP = 32   # values of one scale
+_CODE_BITS = {torch.int8: 8, torch.uint8: 4}
 
 
 class gdn_scan_shape(ctypes.Structure):
@@ -136,17 +137,20 @@ def _gates(like, g, beta, dev):
     """g and beta as rows of one stride each, after checking them against the [B,T,D]
     dims and dtype of ``like``; their dtype code."""
     dims, dtype = like
-    if g.shape != dims or (g.dtype != dtype and g.dtype != torch.float32):
+    gdtype = g.dtype
+    if g.shape != dims or (gdtype != dtype and gdtype != torch.float32):
         raise ValueError(f"g must be {list(dims)} in {dtype} or float32")
     if g.get_device() != dev or (beta is not None and beta.get_device() != dev):
         raise ValueError(f"g and beta must be on cuda:{dev}")
-    g, gs = _row_stride(g)
-    bs = gs
+    gs = bs = dims[2]
+    if not g.is_contiguous():
+        g, gs = _row_stride(g)
     if beta is not None:
-        if beta.shape != dims or beta.dtype != g.dtype:
+        if beta.shape != dims or beta.dtype != gdtype:
             raise ValueError(f"beta must be {list(dims)} in g's dtype")
-        beta, bs = _row_stride(beta)
-    return g, gs, beta, bs, _DTYPES[g.dtype]
+        if not beta.is_contiguous():
+            beta, bs = _row_stride(beta)
+    return g, gs, beta, bs, _DTYPES[gdtype]
 
 
 def _scan_args(x, g, beta, cu_seqlens):
@@ -160,10 +164,12 @@ def _scan_args(x, g, beta, cu_seqlens):
     if (B | T | D) >> 31 or not D:
         raise ValueError("x must be [B,T,D] with sizes below 2^31 and D at least 1")
     g, gs, beta, bs, gcode = _gates((dims, x.dtype), g, beta, dev)
-    N = _sequences(dev, B, cu_seqlens)
+    N, xs = B, D
     if cu_seqlens is not None:
+        N = _sequences(dev, B, cu_seqlens)
         cu_seqlens = cu_seqlens.contiguous()
-    x, xs = _row_stride(x)
+    if not x.is_contiguous():
+        x, xs = _row_stride(x)
     return dev, x, g, beta, cu_seqlens, gdn_scan_shape(B, T, D, N, code, gcode, xs, gs, bs), N
 
 
@@ -438,29 +444,33 @@ def make_state_cache(state_pool, slots, bits=8):
 def _cache_args(pool, pool_indices, codes, scales, cache_indices):
     """Checks a cache against a pool; the device, the structs and what they point to."""
     dev, code = _gpu(pool, "state_pool")
-    if pool.dim() < 2 or not pool.is_contiguous() or pool.shape[0] == 0:
+    dims = pool.shape
+    P = dims[0] if len(dims) > 1 else 0
+    if not P or not pool.is_contiguous():
         raise ValueError("state_pool must be a contiguous [P,...]")
-    P = pool.shape[0]
     E = pool.numel() // P
     if not 0 < E < 1 << 31 or P >> 31:
         raise ValueError("state_pool must have fewer than 2^31 slots of 1 to 2^31 - 1 elements")
-    bits = {torch.int8: 8, torch.uint8: 4}.get(codes.dtype)
-    if bits is None or codes.dim() != 2 or codes.shape[1] != (E if bits == 8 else (E + 1) // 2) \
-            or not codes.is_contiguous():
+    bits = _CODE_BITS.get(codes.dtype)
+    dims = codes.shape
+    if bits is None or len(dims) != 2 or dims[1] != (E if bits == 8 else (E + 1) // 2) or not codes.is_contiguous():
         raise ValueError(f"codes must be a contiguous int8 [slots,{E}] (8 bits) or uint8 [slots,{(E + 1) // 2}] (4 bits)")
-    C = codes.shape[0]
-    if scales.shape != (C, -(-E // GROUP)) or scales.dtype != torch.bfloat16 or not scales.is_contiguous():
-        raise ValueError(f"scales must be a contiguous bfloat16 [{C},{-(-E // GROUP)}]")
+    C, groups = dims[0], -(-E // GROUP)
+    if scales.shape != (C, groups) or scales.dtype != torch.bfloat16 or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous bfloat16 [{C},{groups}]")
     if C >> 31:
         raise ValueError("codes must have fewer than 2^31 slots")
-    for t, name in ((pool_indices, "state_indices"), (cache_indices, "cache_indices")):
-        if t.dim() != 1 or t.dtype != torch.int32 or t.shape != pool_indices.shape:
-            raise ValueError(f"{name} must be int32 [n], the same n for both")
+    n, i32 = pool_indices.shape, torch.int32
+    if len(n) != 1 or pool_indices.dtype != i32 or cache_indices.dtype != i32 or cache_indices.shape != n:
+        raise ValueError("state_indices and cache_indices must be int32 [n], the same n for both")
     if not codes.get_device() == scales.get_device() == pool_indices.get_device() == cache_indices.get_device() == dev:
         raise ValueError(f"codes, scales and the indices must be on cuda:{dev}")
-    pool_indices, cache_indices = pool_indices.contiguous(), cache_indices.contiguous()
-    shape = gdn_held_shape(pool_indices.shape[0], E, E, P, C, code, bits)
-    return dev, gdn_held(codes.data_ptr(), scales.data_ptr()), shape, pool_indices, cache_indices
+    p, c, s = pool.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    p1, c1, s1 = p + P * E * (4 if code else 2), c + C * dims[1], s + 2 * C * groups
+    if (p < c1 and c < p1) or (p < s1 and s < p1) or (c < s1 and s < c1):
+        raise ValueError("state_pool, codes and scales must not overlap")
+    return (dev, gdn_held(c, s), gdn_held_shape(n[0], E, E, P, C, code, bits), pool_indices.contiguous(),
+            cache_indices.contiguous(), p)
 
 
 def state_cache_write(state_pool, state_indices, codes, scales, cache_indices):
@@ -471,9 +481,8 @@ def state_cache_write(state_pool, state_indices, codes, scales, cache_indices):
     outside its tensor is skipped; no cache slot may be named twice.  The format is
     checkpoint_activation's, in groups of 32 elements of the flattened state; with 4
     bits the integers reach from -7 to 7."""
-    dev, held, shape, pi, ci = _cache_args(state_pool, state_indices, codes, scales, cache_indices)
-    _apart("the cache", [codes, scales], state_pool)
-    _run(dev, (_lib or _load()).gdn_hold, state_pool.data_ptr(), pi.data_ptr(), _addr(held), ci.data_ptr(),
+    dev, held, shape, pi, ci, pool = _cache_args(state_pool, state_indices, codes, scales, cache_indices)
+    _run(dev, (_lib or _load()).gdn_hold, pool, pi.data_ptr(), _addr(held), ci.data_ptr(),
          _addr(shape))
 
 
@@ -481,9 +490,8 @@ def state_cache_read(codes, scales, cache_indices, state_pool, state_indices):
     """Reads states back: slot cache_indices[i] of the cache goes to slot
     state_indices[i] of state_pool, rounded once to its dtype.  Indices as for
     state_cache_write; no pool slot may be named twice."""
-    dev, held, shape, pi, ci = _cache_args(state_pool, state_indices, codes, scales, cache_indices)
-    _apart("state_pool", [state_pool], codes, scales)
-    _run(dev, (_lib or _load()).gdn_restore, _addr(held), ci.data_ptr(), state_pool.data_ptr(), pi.data_ptr(),
+    dev, held, shape, pi, ci, pool = _cache_args(state_pool, state_indices, codes, scales, cache_indices)
+    _run(dev, (_lib or _load()).gdn_restore, _addr(held), ci.data_ptr(), pool, pi.data_ptr(),
          _addr(shape))
 
 
