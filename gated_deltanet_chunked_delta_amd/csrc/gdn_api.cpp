@@ -563,13 +563,14 @@ int hold(void *values, const int32_t *value_index, const gdn_held *held, const i
     if (s.n == 0) return GDN_OK;
     if (s.stride < s.D || s.stride > ((int64_t)1 << 31)) return GDN_ERR_SHAPE;
     if ((!value_index && s.n > s.value_rows) || (!held_index && s.n > s.held_rows)) return GDN_ERR_SHAPE;
-    if (s.n > kMaxGrid || gdn::quant_grid(s.n, s.D) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (s.n > INT_MAX) return GDN_ERR_SHAPE;
     if (!values) return GDN_ERR_NULL;
     const int st = check_held(held, true);
     if (st != GDN_OK) return st;
     if (misaligned(s.dtype, values) || misaligned(GDN_F32, value_index, held_index)) return GDN_ERR_ALIGN;
     const gdn::QuantParams p{values, held_of(*held), value_index, held_index, s.n, s.D, s.stride, s.value_rows,
                              s.held_rows};
+    if (gdn::quant_grid(p, s.dtype, s.bits) > kMaxGrid) return GDN_ERR_SHAPE;
     const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
         return gdn::launch_quant(p, s.dtype, s.bits, back, (hipStream_t)stream, prof);
     });

@@ -13,7 +13,7 @@ namespace {
 
 using namespace dev;
 
-// Eight values a thread and part, U parts in flight; four threads a group.
+// Eight values a thread, four threads a group; U of these parts a thread in flight.
 constexpr int kThreads = 256, kPart = kThreads * 8;
 
 // Rows of a tensor, or -1 for a row that is skipped.
@@ -23,26 +23,57 @@ __device__ __forceinline__ int64_t row_at(const int32_t *index, int64_t i, int r
     return r >= 0 && r < rows ? r : -1;
 }
 
-template <typename E, int BITS, int U, bool STREAM>
-__global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p, int tiles) {
-    constexpr int TOP = BITS == 8 ? 127 : 7;
-    const int64_t i = blockIdx.x / tiles;
-    const int64_t from = row_at(p.value_index, i, p.value_rows), to = row_at(p.held_index, i, p.held_rows);
-    if (from < 0 || to < 0) return;
-    const int64_t at = (int64_t)(blockIdx.x % tiles) * (U * kPart) + threadIdx.x * 8;
-    const bool tails = p.D % 8 != 0;
-    const E *src = (const E *)p.values + from * p.stride;
-    typename Raw8<E>::T r[U];
-    int n[U];
+// A thread's parts: U parts of one row (tiles: workgroups a row), or, ROWS, a part of
+// each of U rows (lanes: threads a row, 2^lanes).
+struct Part {
+    int64_t from, to, col;                             // rows of the tensor read and the one written, the first value
+    int n;                                             // values, 0 for a part that is skipped
+};
+template <int U, bool ROWS>
+__device__ __forceinline__ void parts_of(const QuantParams &p, int split, const int32_t *read, int read_rows,
+                                         const int32_t *written, int written_rows, Part (&q)[U]) {
+    if constexpr (ROWS) {
+        const int per = kThreads >> split;             // rows a workgroup and part
+        const int64_t first = (int64_t)blockIdx.x * (U * per) + (threadIdx.x >> split);
+        const int64_t col = (threadIdx.x & ((1 << split) - 1)) * 8;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t i = first + k * per;
+            q[k] = {-1, -1, col, 0};
+            if (i >= p.n) continue;
+            q[k].from = row_at(read, i, read_rows);
+            q[k].to = row_at(written, i, written_rows);
+        }
+    } else {
+        const int64_t i = blockIdx.x / split, at = (int64_t)(blockIdx.x % split) * (U * kPart) + threadIdx.x * 8;
+        const int64_t from = row_at(read, i, read_rows), to = row_at(written, i, written_rows);
+#pragma unroll
+        for (int k = 0; k < U; ++k) q[k] = {from, to, at + k * kPart, 0};
+    }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        n[k] = (int)min(max(p.D - at - k * kPart, (int64_t)0), (int64_t)8);
-        r[k] = load_n<E, 8, STREAM>(src + at + k * kPart, n[k], tails);
+        q[k].n = (int)min(max(p.D - q[k].col, (int64_t)0), (int64_t)8);
+        if (ROWS && (q[k].from < 0 || q[k].to < 0)) q[k].n = 0;
     }
+}
+template <int U, bool ROWS> __device__ __forceinline__ bool skipped(const Part (&q)[U]) {
+    return !ROWS && (q[0].from < 0 || q[0].to < 0);
+}
+
+template <typename E, int BITS, int U, bool STREAM, bool ROWS>
+__global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p, int split) {
+    constexpr int TOP = BITS == 8 ? 127 : 7;
+    Part q[U];
+    parts_of<U, ROWS>(p, split, p.value_index, p.value_rows, p.held_index, p.held_rows, q);
+    if (skipped<U, ROWS>(q)) return;
+    const bool tails = p.D % 8 != 0;
+    typename Raw8<E>::T r[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+        r[k] = load_n<E, 8, STREAM>((const E *)p.values + q[k].from * p.stride + q[k].col, q[k].n, tails);
     const int64_t groups = (p.D + kGroup - 1) / kGroup;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const int64_t col = at + k * kPart;
         float v[8];
         uint32_t high = 0, c[8];
 #pragma unroll
@@ -55,54 +86,50 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p, int tile
         const float s = held_scale<TOP>(high), inv = held_inverse(s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) c[e] = held_code<E>(v[e], s, inv);
-        if (n[k] > 0 && threadIdx.x % 4 == 0) ((bf16 *)p.held.scales)[to * groups + col / kGroup] = (bf16)s;
+        if (q[k].n > 0 && threadIdx.x % 4 == 0) ((bf16 *)p.held.scales)[q[k].to * groups + q[k].col / kGroup] = (bf16)s;
         if constexpr (BITS == 8) {
-            if (n[k] == 8 || tails)
-                store_codes<STREAM>((uint8_t *)p.held.codes + to * p.D + col, pack4(c), pack4(c + 4), n[k]);
+            if (q[k].n == 8 || tails)
+                store_codes<STREAM>((uint8_t *)p.held.codes + q[k].to * p.D + q[k].col, pack4(c), pack4(c + 4), q[k].n);
         } else {
-            uint8_t *dst = (uint8_t *)p.held.codes + to * ((p.D + 1) / 2) + col / 2;
+            uint8_t *dst = (uint8_t *)p.held.codes + q[k].to * ((p.D + 1) / 2) + q[k].col / 2;
             uint32_t w = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) w |= (c[e] & 15u) << (4 * e);
-            if (n[k] == 8) {
+            if (q[k].n == 8) {
                 if constexpr (STREAM)
                     __builtin_nontemporal_store(w, (u32u *)dst);
                 else
                     *(u32u *)dst = w;
             } else {
-                for (int e = 0; e < n[k]; e += 2) dst[e / 2] = (uint8_t)(w >> (4 * e));
+                for (int e = 0; e < q[k].n; e += 2) dst[e / 2] = (uint8_t)(w >> (4 * e));
             }
         }
     }
 }
 
-template <typename E, int BITS, int U, bool STREAM>
-__global__ void __launch_bounds__(kThreads) dequant_kernel(QuantParams p, int tiles) {
-    const int64_t i = blockIdx.x / tiles;
-    const int64_t to = row_at(p.value_index, i, p.value_rows), from = row_at(p.held_index, i, p.held_rows);
-    if (from < 0 || to < 0) return;
-    const int64_t at = (int64_t)(blockIdx.x % tiles) * (U * kPart) + threadIdx.x * 8;
+template <typename E, int BITS, int U, bool STREAM, bool ROWS>
+__global__ void __launch_bounds__(kThreads) dequant_kernel(QuantParams p, int split) {
+    Part q[U];
+    parts_of<U, ROWS>(p, split, p.held_index, p.held_rows, p.value_index, p.value_rows, q);
+    if (skipped<U, ROWS>(q)) return;
     const bool tails = p.D % 8 != 0;
-    const bf16 *scales = (const bf16 *)p.held.scales + from * ((p.D + kGroup - 1) / kGroup);
-    const uint8_t *src = (const uint8_t *)p.held.codes + from * (BITS == 8 ? p.D : (p.D + 1) / 2);
+    const int64_t groups = (p.D + kGroup - 1) / kGroup, row = BITS == 8 ? p.D : (p.D + 1) / 2;
     u32x2 w[U];
     float s[U];
-    int n[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const int64_t col = at + k * kPart;
-        n[k] = (int)min(max(p.D - col, (int64_t)0), (int64_t)8);
-        s[k] = n[k] > 0 ? (float)scales[col / kGroup] : 0.f;
+        const uint8_t *src = (const uint8_t *)p.held.codes + q[k].from * row + (BITS == 8 ? q[k].col : q[k].col / 2);
+        s[k] = q[k].n > 0 ? (float)((const bf16 *)p.held.scales)[q[k].from * groups + q[k].col / kGroup] : 0.f;
         w[k] = u32x2{0, 0};
         if constexpr (BITS == 8) {
-            if (n[k] == 8 || tails) w[k] = load_codes<STREAM>(src + col, n[k]);
-        } else if (n[k] == 8) {
+            if (q[k].n == 8 || tails) w[k] = load_codes<STREAM>(src, q[k].n);
+        } else if (q[k].n == 8) {
             if constexpr (STREAM)
-                w[k][0] = __builtin_nontemporal_load((const u32u *)(src + col / 2));
+                w[k][0] = __builtin_nontemporal_load((const u32u *)src);
             else
-                w[k][0] = *(const u32u *)(src + col / 2);
+                w[k][0] = *(const u32u *)src;
         } else {
-            for (int e = 0; e < n[k]; e += 2) w[k][0] |= (uint32_t)src[(col + e) / 2] << (4 * e);
+            for (int e = 0; e < q[k].n; e += 2) w[k][0] |= (uint32_t)src[e / 2] << (4 * e);
         }
     }
 #pragma unroll
@@ -111,46 +138,76 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(QuantParams p, int ti
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             Raw8<E>::set(r, e, (BITS == 8 ? held_byte(w[k][e / 4], e % 4) : (float)((int)(w[k][0] << (28 - 4 * e)) >> 28)) * s[k]);
-        store_n<E, 8, STREAM>((E *)p.values + to * p.stride + at + k * kPart, r, n[k], tails);
+        store_n<E, 8, STREAM>((E *)p.values + q[k].to * p.stride + q[k].col, r, q[k].n, tails);
     }
 }
 
-int64_t tiles_of(int64_t D, int U) { return (D + U * kPart - 1) / (U * kPart); }
-
-// Four parts a workgroup where that leaves every CU eight workgroups, for the loads in
+// What a call of these sizes launches.  Rows that follow each other in both tensors and
+// are of whole groups are one long row (524,288 rows of 128 to 8 bits 33 us, a workgroup
+// each 313); others of up to 1024 values share a workgroup (parts of wider rows 44 and 300
+// us; 65,536 rows of 1000 41 and 50).
+// Four parts a thread where that leaves every CU eight workgroups, for the loads in
 // flight (the 256 states there and back 140 us, with one part and through the cache
 // 168, with eight parts 139); one part for few rows, which then have the more
 // workgroups.  Passes over more than the 256 MiB of the last cache are streamed past
 // it, smaller ones stay there for their reader.
-template <typename E, int BITS, int U, bool STREAM> void launch_u(const QuantParams &p, bool back, hipStream_t st) {
-    const int tiles = (int)tiles_of(p.D, U);
-    const unsigned grid = (unsigned)(p.n * tiles);
-    if (back)
-        dequant_kernel<E, BITS, U, STREAM><<<grid, kThreads, 0, st>>>(p, tiles);
-    else
-        quant_kernel<E, BITS, U, STREAM><<<grid, kThreads, 0, st>>>(p, tiles);
+struct Plan {
+    QuantParams p;
+    bool rows, four, stream;
+    int split;                                         // see Part
+    int64_t grid;
+};
+Plan plan_of(const QuantParams &q, int elem, int bits) {
+    Plan f{q, false, false, false, 0, 0};
+    QuantParams &p = f.p;
+    if (!p.value_index && !p.held_index && (p.n == 1 || (p.stride == p.D && p.D % kGroup == 0))) {
+        p.D *= p.n;
+        p.n = 1;
+        p.stride = p.D;
+    }
+    f.rows = p.D <= kPart / 2 && p.n > 1;
+    f.split = 2;
+    while (f.rows && (8 << f.split) < p.D) ++f.split;
+    const int64_t per = kThreads >> f.split;
+    auto grid = [&](int U) { return f.rows ? (p.n + U * per - 1) / (U * per) : p.n * ((p.D + U * kPart - 1) / (U * kPart)); };
+    f.four = (f.rows || p.D >= 4 * kPart) && grid(4) >= 2048;
+    f.stream = f.four && (double)p.n * p.D * (elem + bits / 8.0) > (256 << 20);
+    f.grid = grid(f.four ? 4 : 1);
+    if (!f.rows) f.split = (int)(f.grid / p.n);
+    return f;
 }
-template <typename E, int BITS> void launch_e(const QuantParams &p, bool back, hipStream_t st) {
-    if (p.D < 4 * kPart || p.n * tiles_of(p.D, 4) < 2048)
-        launch_u<E, BITS, 1, false>(p, back, st);
-    else if ((double)p.n * p.D * (sizeof(E) + BITS / 8.0) > (256 << 20))
-        launch_u<E, BITS, 4, true>(p, back, st);
+
+template <typename E, int BITS, int U, bool STREAM, bool ROWS> void launch_rows(const Plan &f, bool back, hipStream_t st) {
+    if (back)
+        dequant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
     else
-        launch_u<E, BITS, 4, false>(p, back, st);
+        quant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
+}
+template <typename E, int BITS, int U, bool STREAM> void launch_u(const Plan &f, bool back, hipStream_t st) {
+    f.rows ? launch_rows<E, BITS, U, STREAM, true>(f, back, st) : launch_rows<E, BITS, U, STREAM, false>(f, back, st);
+}
+template <typename E, int BITS> void launch_e(const Plan &f, bool back, hipStream_t st) {
+    if (!f.four)
+        launch_u<E, BITS, 1, false>(f, back, st);
+    else if (f.stream)
+        launch_u<E, BITS, 4, true>(f, back, st);
+    else
+        launch_u<E, BITS, 4, false>(f, back, st);
 }
 
 }  // namespace
 
-int64_t quant_grid(int64_t n, int64_t D) { return n * tiles_of(D, 1); }
+int64_t quant_grid(const QuantParams &p, int dtype, int bits) { return plan_of(p, dtype == 0 ? 2 : 4, bits).grid; }
 
 hipError_t launch_quant(const QuantParams &p, int dtype, int bits, bool back, hipStream_t stream, Profiler *prof) {
     if (p.n == 0 || p.D == 0) return hipSuccess;
+    const Plan f = plan_of(p, dtype == 0 ? 2 : 4, bits);
     const int kind = back ? kDequantKernel : kQuantKernel;
     if (prof) prof->begin(kind, stream);
     if (dtype == 0)
-        bits == 8 ? launch_e<bf16, 8>(p, back, stream) : launch_e<bf16, 4>(p, back, stream);
+        bits == 8 ? launch_e<bf16, 8>(f, back, stream) : launch_e<bf16, 4>(f, back, stream);
     else
-        bits == 8 ? launch_e<float, 8>(p, back, stream) : launch_e<float, 4>(p, back, stream);
+        bits == 8 ? launch_e<float, 8>(f, back, stream) : launch_e<float, 4>(f, back, stream);
     const hipError_t err = hipGetLastError();
     if (prof) prof->end(kind, stream);
     return err;

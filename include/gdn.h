@@ -749,7 +749,7 @@ typedef struct gdn_held_shape {
  * Values and scales are aligned to their element (GDN_ERR_ALIGN), codes need no
  * alignment.  The tensors must not overlap.  Returns GDN_OK, GDN_ERR_NULL,
  * GDN_ERR_SHAPE (also n above value_rows or held_rows without that side's index, or
- * too many rows for one launch: 2^24 - 1 blocks of 2048 values), GDN_ERR_DTYPE,
+ * 2^31 rows, or too many values for one launch: 2^24 - 1 blocks of 8192), GDN_ERR_DTYPE,
  * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
 int gdn_hold(const void *values, const int32_t *value_index, const gdn_held *held, const int32_t *held_index,
              const gdn_held_shape *shape, void *stream);

@@ -169,6 +169,51 @@ def test_state_cache_slot_beyond_32_bits():
     assert torch.equal(pool[P - 1], back[0]) and not pool[:P - 1].any()
 
 
+@TYPES
+@pytest.mark.parametrize("rows,D", [(540_000, 7), (270_000, 33), (66_000, 100), (40_000, 1000), (20_000, 1001), (70_000, 1002)])
+def test_many_short_rows(rows, D, dtype):
+    """Rows that share a workgroup, several a thread: each is what a call on a few rows makes of it."""
+    gdn = _gdn()
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    wide = torch.randn(rows, D + 3, device=DEV, generator=gen, dtype=F32).to(dtype)
+    x = wide[:, 2:D + 2]
+    c = gdn.checkpoint_activation(x)
+    back = gdn.restore_activation(c, dtype)
+    for at in (0, 255, rows // 3, rows - 1000, rows - 7):
+        few = slice(at, min(at + 300, rows))
+        codes, scales = orc.hold(x[few].cpu())
+        assert (c.codes[few].cpu().numpy() == codes).all() and (_np(c.scales[few]) == scales).all()
+        assert torch.equal(back[few].cpu(), torch.from_numpy(orc.restore(codes, scales)).to(F32).to(dtype))
+    # the same through a pool's slots in another order, with pairs that are skipped, to 4 bits
+    pool = x.contiguous()
+    codes, scales = gdn.make_state_cache(pool, rows, 4)
+    perm = torch.randperm(rows, device=DEV, generator=gen).to(torch.int32)
+    src = torch.arange(rows, device=DEV, dtype=torch.int32)
+    src[5::11] = -1
+    gdn.state_cache_write(pool, src, codes, scales, perm)
+    other = torch.full_like(pool, 9.0)
+    gdn.state_cache_read(codes, scales, perm, other, src)
+    assert (other[5::11] == 9.0).all() and not codes[perm[5::11].long()].any()
+    for at in (0, rows // 2, rows - 300):
+        held = orc.hold(pool[at:at + 300].cpu(), 4)
+        want = torch.from_numpy(orc.restore(*held)).to(F32).to(dtype)
+        keep = src[at:at + 300].cpu() >= 0
+        assert torch.equal(other[at:at + 300].cpu()[keep], want[keep])
+
+
+def test_more_rows_than_a_launch_has_workgroups():
+    """2^24 + 3 rows of a head: rows that follow each other are one."""
+    gdn = _gdn()
+    n = (1 << 24) + 3
+    x = torch.randn(n, 128, device=DEV, dtype=BF)
+    c = gdn.checkpoint_activation(x)
+    back = gdn.restore_activation(c)
+    for at in (0, 1 << 20, n - 200):
+        codes, scales = orc.hold(x[at:at + 200].cpu())
+        assert (c.codes[at:at + 200].cpu().numpy() == codes).all() and (_np(c.scales[at:at + 200]) == scales).all()
+        assert torch.equal(back[at:at + 200].cpu(), torch.from_numpy(orc.restore(codes, scales)).to(F32).to(BF))
+
+
 NORMS = [((5, 4), 128), ((3, 1, 6), 64), ((7,), 1), ((2, 3), 100), ((9, 2), 129), ((3,), 512), ((2, 2), 777),
          ((2,), 1024), ((300, 32), 128), ((3, 5), 1021), ((700, 9), 5), ((90, 10), 187), ((70, 3), 9), ((500, 7), 96)]
 

@@ -117,7 +117,7 @@ def _hold(entry, shape=None, no_shape=False, no_held=False, **ptr):
     (dict(shape=dict(n=-1)), -2), (dict(shape=dict(D=0)), -2), (dict(shape=dict(D=1 << 31)), -2),
     (dict(shape=dict(stride=99)), -2), (dict(shape=dict(stride=(1 << 31) + 1)), -2), (dict(shape=dict(value_rows=-1)), -2),
     (dict(shape=dict(n=10), value_index=None), -2), (dict(shape=dict(n=8), held_index=None), -2),
-    (dict(shape=dict(n=1 << 24)), -2), (dict(shape=dict(n=1 << 20, D=1 << 20, stride=1 << 20)), -2),
+    (dict(shape=dict(n=1 << 31)), -2), (dict(shape=dict(n=1 << 20, D=1 << 20, stride=1 << 20)), -2),
     (dict(shape=dict(dtype=2)), -3), (dict(shape=dict(bits=5)), -4), (dict(shape=dict(bits=16)), -4),
     (dict(values=FAKE + 1), -7), (dict(scales=FAKE + 1), -7), (dict(value_index=FAKE + 2), -7), (dict(held_index=FAKE + 1), -7),
     (dict(shape=dict(n=0)), 0),
