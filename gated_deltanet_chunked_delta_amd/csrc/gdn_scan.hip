@@ -135,8 +135,10 @@ constexpr int kGroupTiles = 8, kBlockGroups = 8;   // tiles of a group, groups o
 template <int R> __device__ __forceinline__ int strip_int(int x) { return R == 1 ? __builtin_amdgcn_readfirstlane(x) : x; }
 
 // Channels of a lane.  The vectors of VC channels are shared out evenly among the
-// column blocks; the last one of an odd row ends with it and overlaps its neighbour,
-// which is in the same strip: both compute and store the same values.
+// column blocks, 16 at a time, so that blocks meet where lines or halves of them do
+// (gradients of 96,712 tokens of 720 channels with fp32 gates 398 -> 355 us); the last
+// vector of an odd row ends with it and overlaps its neighbour, which is in the same
+// strip: both compute and store the same values.
 struct Lane {
     uint32_t c;                                        // unsigned: a 32-bit offset from a row in scalar registers
     bool live;
@@ -148,9 +150,9 @@ template <typename E> __device__ __forceinline__ E *at(void *base, int64_t row, 
     return (E *)((char *)((E *)base + row * stride) + c * (uint32_t)sizeof(E));
 }
 template <int VC> __device__ __forceinline__ Lane lane_of(int D, int ncb, int cb, int lane) {
-    const int nv = (D + VC - 1) / VC, each = nv / ncb, more = nv % ncb;
-    const int v = cb * each + min(cb, more) + lane;
-    return {(uint32_t)min(v * VC, D - VC), lane < each + (cb < more ? 1 : 0)};
+    const int nv = (D + VC - 1) / VC, units = (nv + 15) / 16, each = units / ncb, more = units % ncb;
+    const int v = 16 * (cb * each + min(cb, more)) + lane;
+    return {(uint32_t)min(v * VC, D - VC), v < nv && lane < 16 * (each + (cb < more ? 1 : 0))};
 }
 template <int VC> __host__ __device__ __forceinline__ int column_blocks(int D) { return ((D + VC - 1) / VC + 63) / 64; }
 
@@ -839,11 +841,16 @@ int64_t row_words(int D, const Tile &t) { return (int64_t)blocks_of(D, t) * t.VC
 
 // Passes over more than the 256 MiB of the last cache are streamed past it: packed
 // prompts 645 against 699 us, gradients of 16,384 tokens 286 against 311; smaller ones
-// lose by it (2042 tokens of 1001 channels 22.4 against 21.2 us).
+// lose by it (2042 tokens of 1001 channels 22.4 against 21.2 us).  So do rows that are
+// not of whole lines, of which two workgroups read and write a part each: 96,712 tokens
+// of 721 channels with bf16 gates 183 against 171 us, backward 350 against 304, with fp32
+// gates 433 against 398 (720 channels: 170 and 169, 298 and 278, 356 and 358); only the
+// forward pass with fp32 gates keeps a gain (213 against 217, 204 against 211).
 template <typename E, typename G> bool streams(const ScanParams &p, Pass pass) {
     const int gates = p.beta ? 2 : 1, kept = p.y8.codes ? gates : gates * (int)sizeof(E);
     const int token = pass == kForward ? 2 * sizeof(E) + gates * sizeof(G) : 2 * sizeof(E) + 2 * gates * sizeof(G) + kept;
-    return (int64_t)p.T_tot * p.D * token > 256 << 20;
+    const bool lines = p.D * sizeof(E) % 128 == 0 || (pass == kForward && sizeof(G) == 4);
+    return lines && (int64_t)p.T_tot * p.D * token > 256 << 20;
 }
 template <typename E, typename G, bool BETA, bool HELD, Width WIDTH> void launch_tiles(const ScanParams &p, Pass pass, hipStream_t st, Profiler *prof) {
     constexpr Tile f = tile_of(WIDTH, {false, sizeof(E) == 4, sizeof(G) == 4, BETA, HELD});
