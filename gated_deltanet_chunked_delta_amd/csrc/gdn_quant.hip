@@ -23,49 +23,38 @@ __device__ __forceinline__ int64_t row_at(const int32_t *index, int64_t i, int r
     return r >= 0 && r < rows ? r : -1;
 }
 
-// A thread's parts: U parts of one row (tiles: workgroups a row), or, ROWS, a part of
-// each of U rows (lanes: threads a row, 2^lanes).
+// A thread's parts: U parts of one row (split: workgroups a row), or, ROWS, one of a row
+// that it shares with 2^split - 1 others.
 struct Part {
     int64_t from, to, col;                             // rows of the tensor read and the one written, the first value
-    int n;                                             // values, 0 for a part that is skipped
+    int n;                                             // values
 };
+// False where there is nothing to do.  Four neighbours stay together: they share a row.
 template <int U, bool ROWS>
-__device__ __forceinline__ void parts_of(const QuantParams &p, int split, const int32_t *read, int read_rows,
+__device__ __forceinline__ bool parts_of(const QuantParams &p, int split, const int32_t *read, int read_rows,
                                          const int32_t *written, int written_rows, Part (&q)[U]) {
+    static_assert(!ROWS || U == 1, "a thread takes one row");
+    int64_t i, at;
     if constexpr (ROWS) {
-        const int per = kThreads >> split;             // rows a workgroup and part
-        const int64_t first = (int64_t)blockIdx.x * (U * per) + (threadIdx.x >> split);
-        const int64_t col = (threadIdx.x & ((1 << split) - 1)) * 8;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int64_t i = first + k * per;
-            q[k] = {-1, -1, col, 0};
-            if (i >= p.n) continue;
-            q[k].from = row_at(read, i, read_rows);
-            q[k].to = row_at(written, i, written_rows);
-        }
+        i = (int64_t)blockIdx.x * (kThreads >> split) + (threadIdx.x >> split);
+        at = (threadIdx.x & ((1 << split) - 1)) * 8;
+        if (i >= p.n) return false;
     } else {
-        const int64_t i = blockIdx.x / split, at = (int64_t)(blockIdx.x % split) * (U * kPart) + threadIdx.x * 8;
-        const int64_t from = row_at(read, i, read_rows), to = row_at(written, i, written_rows);
-#pragma unroll
-        for (int k = 0; k < U; ++k) q[k] = {from, to, at + k * kPart, 0};
+        i = blockIdx.x / split;
+        at = (int64_t)(blockIdx.x % split) * (U * kPart) + threadIdx.x * 8;
     }
+    const int64_t from = row_at(read, i, read_rows), to = row_at(written, i, written_rows);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        q[k].n = (int)min(max(p.D - q[k].col, (int64_t)0), (int64_t)8);
-        if (ROWS && (q[k].from < 0 || q[k].to < 0)) q[k].n = 0;
-    }
-}
-template <int U, bool ROWS> __device__ __forceinline__ bool skipped(const Part (&q)[U]) {
-    return !ROWS && (q[0].from < 0 || q[0].to < 0);
+    for (int k = 0; k < U; ++k)
+        q[k] = {from, to, at + k * kPart, (int)min(max(p.D - at - k * kPart, (int64_t)0), (int64_t)8)};
+    return from >= 0 && to >= 0;
 }
 
 template <typename E, int BITS, int U, bool STREAM, bool ROWS>
 __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p, int split) {
     constexpr int TOP = BITS == 8 ? 127 : 7;
     Part q[U];
-    parts_of<U, ROWS>(p, split, p.value_index, p.value_rows, p.held_index, p.held_rows, q);
-    if (skipped<U, ROWS>(q)) return;
+    if (!parts_of<U, ROWS>(p, split, p.value_index, p.value_rows, p.held_index, p.held_rows, q)) return;
     const bool tails = p.D % 8 != 0;
     typename Raw8<E>::T r[U];
 #pragma unroll
@@ -110,8 +99,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantParams p, int spli
 template <typename E, int BITS, int U, bool STREAM, bool ROWS>
 __global__ void __launch_bounds__(kThreads) dequant_kernel(QuantParams p, int split) {
     Part q[U];
-    parts_of<U, ROWS>(p, split, p.held_index, p.held_rows, p.value_index, p.value_rows, q);
-    if (skipped<U, ROWS>(q)) return;
+    if (!parts_of<U, ROWS>(p, split, p.held_index, p.held_rows, p.value_index, p.value_rows, q)) return;
     const bool tails = p.D % 8 != 0;
     const int64_t groups = (p.D + kGroup - 1) / kGroup, row = BITS == 8 ? p.D : (p.D + 1) / 2;
     u32x2 w[U];
@@ -144,10 +132,10 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(QuantParams p, int sp
 
 // What a call of these sizes launches.  Rows that follow each other in both tensors and
 // are of whole groups are one long row (524,288 rows of 128 to 8 bits 33 us, a workgroup
-// each 313); others of up to 1024 values share a workgroup (parts of wider rows 44 and 300
-// us; 65,536 rows of 1000 41 and 50).
-// Four parts a thread where that leaves every CU eight workgroups, for the loads in
-// flight (the 256 states there and back 140 us, with one part and through the cache
+// each 313); others of up to 1024 values share a workgroup, a part a thread (parts of wider
+// rows 38 and 300 us; 65,536 rows of 1000 35 and 50; with four parts a thread 44 and 41).
+// Of long rows four parts a thread where that leaves every CU eight workgroups, for the
+// loads in flight (256 states there and back 139 us, with one part and through the cache
 // 168, with eight parts 139); one part for few rows, which then have the more
 // workgroups.  Passes over more than the 256 MiB of the last cache are streamed past
 // it, smaller ones stay there for their reader.
@@ -169,30 +157,29 @@ Plan plan_of(const QuantParams &q, int elem, int bits) {
     f.split = 2;
     while (f.rows && (8 << f.split) < p.D) ++f.split;
     const int64_t per = kThreads >> f.split;
-    auto grid = [&](int U) { return f.rows ? (p.n + U * per - 1) / (U * per) : p.n * ((p.D + U * kPart - 1) / (U * kPart)); };
-    f.four = (f.rows || p.D >= 4 * kPart) && grid(4) >= 2048;
+    auto grid = [&](int U) { return f.rows ? (p.n + per - 1) / per : p.n * ((p.D + U * kPart - 1) / (U * kPart)); };
+    f.four = !f.rows && p.D >= 4 * kPart && grid(4) >= 2048;
     f.stream = f.four && (double)p.n * p.D * (elem + bits / 8.0) > (256 << 20);
     f.grid = grid(f.four ? 4 : 1);
     if (!f.rows) f.split = (int)(f.grid / p.n);
     return f;
 }
 
-template <typename E, int BITS, int U, bool STREAM, bool ROWS> void launch_rows(const Plan &f, bool back, hipStream_t st) {
+template <typename E, int BITS, int U, bool STREAM, bool ROWS> void launch(const Plan &f, bool back, hipStream_t st) {
     if (back)
         dequant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
     else
         quant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
 }
-template <typename E, int BITS, int U, bool STREAM> void launch_u(const Plan &f, bool back, hipStream_t st) {
-    f.rows ? launch_rows<E, BITS, U, STREAM, true>(f, back, st) : launch_rows<E, BITS, U, STREAM, false>(f, back, st);
-}
 template <typename E, int BITS> void launch_e(const Plan &f, bool back, hipStream_t st) {
-    if (!f.four)
-        launch_u<E, BITS, 1, false>(f, back, st);
+    if (f.rows)
+        launch<E, BITS, 1, false, true>(f, back, st);
+    else if (!f.four)
+        launch<E, BITS, 1, false, false>(f, back, st);
     else if (f.stream)
-        launch_u<E, BITS, 4, true>(f, back, st);
+        launch<E, BITS, 4, true, false>(f, back, st);
     else
-        launch_u<E, BITS, 4, false>(f, back, st);
+        launch<E, BITS, 4, false, false>(f, back, st);
 }
 
 }  // namespace
