@@ -351,11 +351,12 @@ def gated_linear_recurrence_bwd(x, g, y, dy, beta=None, dht=None, initial_state=
 def _held_rows(c, rows, D, dev, name):
     """A checkpoint of rows of D values: its tensors, contiguous, and the struct."""
     codes, scales = c
+    dims = codes.shape
     if codes.dtype != torch.int8 or scales.dtype != torch.bfloat16:
         raise ValueError(f"{name}: a checkpoint has int8 codes and bfloat16 scales")
     if codes.numel() != rows * D or scales.numel() != rows * -(-D // GROUP):
         raise ValueError(f"{name}: codes and scales must be those of {rows} rows of {D} values")
-    if codes.dim() == 0 or (codes.shape[-1] != D and (D % GROUP or codes.shape[-1] % GROUP)):
+    if not dims or (dims[-1] != D and (D % GROUP or dims[-1] % GROUP)):
         raise ValueError(f"{name}: a checkpoint of other rows than {D} values needs both in whole groups of {GROUP}")
     if codes.get_device() != dev or scales.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}")
@@ -372,8 +373,9 @@ def _device(t):
 
 def _new_checkpoint(x):
     dims = x.shape
-    return Checkpoint(x.new_empty(dims, dtype=torch.int8),
-                      x.new_empty((*dims[:-1], -(-dims[-1] // GROUP)), dtype=torch.bfloat16))
+    codes = torch.empty_like(x, dtype=torch.int8) if x.is_contiguous() else x.new_empty(dims, dtype=torch.int8)
+    groups = (*dims[:-1], -(-dims[-1] // GROUP))
+    return Checkpoint(codes, x.new_empty(groups) if x.dtype == torch.bfloat16 else x.new_empty(groups, dtype=torch.bfloat16))
 
 
 def checkpoint_activation(x):
@@ -510,8 +512,9 @@ def fused_gated_rms_norm_checkpoint(x, z, weight, eps=1e-6, out=None):
         out = torch.empty_like(x)
     else:
         _apart("out", [_given(out, x.shape, x, dev, "out")], weight, x, z)
-    cx, cz = _new_checkpoint(x), _new_checkpoint(x)
-    x8, z8 = gdn_held(cx.codes.data_ptr(), cx.scales.data_ptr()), gdn_held(cz.codes.data_ptr(), cz.scales.data_ptr())
+    cx = codes, scales = _new_checkpoint(x)
+    cz = Checkpoint(torch.empty_like(codes), torch.empty_like(scales))   # cheaper than new ones by their sizes
+    x8, z8 = gdn_held(codes.data_ptr(), scales.data_ptr()), gdn_held(cz.codes.data_ptr(), cz.scales.data_ptr())
     _run(dev, (_lib or _load()).gdn_gated_norm_hold, x.data_ptr(), z.data_ptr(), weight.data_ptr(), eps,
          out.data_ptr(), _addr(x8), _addr(z8), _addr(shape))
     return out, cx, cz
