@@ -192,9 +192,13 @@ __global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 4 : 2) norm_held_bwd_ke
     }
 }
 
-// At most as many as norm_bwd_workspace_bytes has rows for.
+// At most as many as norm_bwd_workspace_bytes has rows for; one for rows of two turns,
+// whose sums are dweight then, without a launch for them (32 rows of 128 3.9 us and with
+// two launches 6.1, 64 rows 5.3 and 6.1; 128 rows would take 7.9 and 6.1).
+constexpr int kFewTurns = 2;
 int held_bwd_blocks(int64_t rows, int D) {
     const int gpb = kBwdThreads / split_of(D).L;
+    if (rows <= kFewTurns * gpb) return 1;
     return (int)std::min<int64_t>((rows + gpb - 1) / gpb, norm_bwd_blocks(rows, D));
 }
 template <typename E, int L, int NV, bool STREAM>
@@ -237,13 +241,16 @@ hipError_t launch_norm_held(const NormParams &p, const Held &x8, const Held &z8,
     return err;
 }
 
-hipError_t launch_norm_held_bwd(const NormParams &p, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
+hipError_t launch_norm_held_bwd(const NormParams &q, const Held &x8, const Held &z8, int dtype, hipStream_t stream,
                                 Profiler *prof) {
+    NormParams p = q;
+    const bool one = p.rows > 0 && held_bwd_blocks(p.rows, p.D) == 1;
+    if (one) p.part = p.dweight;
     if (p.rows > 0) {
         if (prof) prof->begin(kNormBwdKernel, stream);
         const hipError_t err = launch_any(p, x8, z8, dtype, true, stream);
         if (prof) prof->end(kNormBwdKernel, stream);
-        if (err != hipSuccess) return err;
+        if (err != hipSuccess || one) return err;
     }
     return launch_column_sum(p.part, p.rows > 0 ? held_bwd_blocks(p.rows, p.D) : 0, p.D, p.dweight, p.D, 0, nullptr,
                              stream, prof);
