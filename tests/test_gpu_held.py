@@ -215,7 +215,8 @@ def test_more_rows_than_a_launch_has_workgroups():
 
 
 NORMS = [((5, 4), 128), ((3, 1, 6), 64), ((7,), 1), ((2, 3), 100), ((9, 2), 129), ((3,), 512), ((2, 2), 777),
-         ((2,), 1024), ((300, 32), 128), ((3, 5), 1021), ((700, 9), 5), ((90, 10), 187), ((70, 3), 9), ((500, 7), 96)]
+         ((2,), 1024), ((300, 32), 128), ((3, 5), 1021), ((700, 9), 5), ((90, 10), 187), ((70, 3), 9), ((500, 7), 96),
+         ((32,), 128), ((8, 8), 128), ((65,), 128), ((17,), 512)]   # one workgroup's turns, and one row more
 
 
 @TYPES
