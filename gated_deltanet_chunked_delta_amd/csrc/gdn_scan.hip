@@ -41,7 +41,9 @@ using namespace dev;
 // to -5 and 5.1 2^-24 to -87, and 0 below: n = the integer nearest to g / ln 2,
 // r = g - n ln 2, e^r = 1 + r + r^2 p(r) with p of degree 4 interpolating at
 // Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n added to the exponent.  The sum
-// g / ln 2 + 1.5 2^23 has n in its low bits.  11 instructions; the hardware
+// g / ln 2 + 1.5 2^23 has n in its low bits.  ldexp adds it: NaN for a NaN whatever its
+// payload (which an integer sum would carry into the exponent), infinity for a gate above
+// 88.7, which has no business here.  12 instructions; the hardware
 // exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on average,
 // which a channel sums over all the tokens that it remembers (it would save 1 to 5 %).
 __device__ __forceinline__ float decay(float g) {
@@ -53,7 +55,7 @@ __device__ __forceinline__ float decay(float g) {
     q = fmaf(r, q, 0.5f);
     q = fmaf(r, q, 1.f);
     q = fmaf(r, q, 1.f);
-    return g < -87.f ? 0.f : __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));   // NaN for a NaN
+    return g < -87.f ? 0.f : __builtin_amdgcn_ldexpf(q, (int)(__float_as_uint(t) - __float_as_uint(kRoundBias)));
 }
 
 // VC = 1, 2 or 4 consecutive elements, as loaded, at any address.  S: past the caches.

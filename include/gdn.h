@@ -647,6 +647,8 @@ int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, 
  * with the gates of the delta rule: g <= 0 in log space, the lowest value of its
  * type or -infinity for a channel that forgets everything, beta the write
  * strength (gdn_gating makes both, for any number of channels).  States are fp32.
+ * g is not checked: a NaN makes the channel's states NaNs from there to the end of its
+ * sequence, a gate above 0 grows them (e^g is infinite above 88.7).
  *
  * Sizes.
  *   B, T, N       as in gdn_shape (with cu_seqlens B = 1)

@@ -1,0 +1,84 @@
+"""The gated linear recurrence at the edges of its numbers: gates that are NaN in any of a
+NaN's bit patterns, above zero, and over the whole range of the decays."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _gdn():
+    import gated_deltanet_chunked_delta_amd as gdn
+    gdn.load_library()
+    return gdn
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(seed, T, D, dtype=F32, gate=F32):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(1, T, D, generator=gen).to(dtype).to(DEV)
+    g = (-torch.nn.functional.softplus(torch.randn(1, T, D, generator=gen)) * 0.2).to(gate).to(DEV)
+    b = torch.rand(1, T, D, generator=gen).to(gate).to(DEV)
+    return x, g, b, torch.randn(1, T, D, generator=gen).to(dtype).to(DEV)
+
+
+def _cu(*lens):
+    return torch.tensor(np.cumsum([0] + list(lens)), dtype=I32, device=DEV)
+
+
+def _bits(pattern):
+    """The fp32 number of these bits, as the int32 that they are."""
+    return int(np.array(pattern, dtype=np.uint32).view(np.int32))
+
+
+@pytest.mark.parametrize("D", [3, 37, 133])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_a_gate_that_is_not_a_number(dtype, D):
+    """The states from a NaN gate on, and the gradients up to it, are NaNs whatever bits the NaN's payload has; other
+    channels and sequences are the bits that they were."""
+    gdn = _gdn()
+    lens, at, ch = (40, 700, 30), 45, D // 2
+    cu, T = _cu(*lens), sum(lens)
+    x, g, b, dy = _inputs(D, T, D, dtype)
+
+    def both(g):
+        y, f = gdn.gated_linear_recurrence(x, g, b, cu_seqlens=cu)
+        return (y, f, *gdn.gated_linear_recurrence_bwd(x, g, y, dy, b, cu_seqlens=cu, output_dinitial=True))
+
+    clean = both(g)
+    for pattern in (0x7fc00000, 0x7fffffff, 0xffffffff, 0x7fc00001, 0xffc001ff, 0x7f800001):
+        bad = g.clone()
+        bad.view(I32)[0, at, ch] = _bits(pattern)
+        y, f, dx, dg, dbeta, dinitial = got = both(bad)
+        assert y[0, at:740, ch].isnan().all() and f[1, ch].isnan(), hex(pattern)
+        assert dx[0, 40:at, ch].isnan().all() and dg[0, 40:at + 1, ch].isnan().all() and dinitial[1, ch].isnan(), hex(pattern)
+        for u, v in zip(got, clean):
+            same = torch.ones_like(u, dtype=torch.bool)
+            if u.dim() == 2:
+                same[1, ch] = False
+            else:
+                same[0, 40:740, ch] = False
+            assert torch.equal(u[same], v[same]), hex(pattern)
+        # a token at a time
+        pool, slots = torch.zeros(2, D, device=DEV), torch.tensor([1, 0], dtype=I32, device=DEV)
+        ys = gdn.gated_linear_recurrence_steps(x[0, 44:48].view(2, 2, D), bad[0, 44:48].view(2, 2, D), pool, slots)
+        assert ys[0, 1, ch].isnan() and pool[1, ch].isnan() and not ys[0, 0].isnan().any(), hex(pattern)
+        ys[0, 1, ch], pool[1, ch] = 0, 0
+        assert ys.isfinite().all() and pool.isfinite().all()
+
+
+def test_a_gate_above_zero():
+    """Not in the gates' range, but no other number than e^g: within its rounding below 88, infinite from 89 on."""
+    gdn = _gdn()
+    g = torch.tensor([1e-3, 0.5, 3.0, 40.0, 88.0, 89.0, 100.0, 1e4, 3e6, 1e10, 1e30], device=DEV).view(1, 1, -1)
+    x, h = torch.zeros_like(g), torch.ones(1, g.shape[-1], device=DEV)
+    y, f = gdn.gated_linear_recurrence(x, g, initial_state=h)
+    assert torch.equal(y[:, 0], f) and (f[0, 5:] == float("inf")).all()
+    # e^g is off by at most 6 2^-24 of itself up to there (see test of the whole range for g <= 0)
+    np.testing.assert_allclose(_np(f)[0, :5], np.exp(_np(g)[0, 0, :5]), rtol=6 * 2.0 ** -24)
