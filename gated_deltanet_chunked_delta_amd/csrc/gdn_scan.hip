@@ -37,18 +37,19 @@ namespace {
 
 using namespace dev;
 
-// e^g for g <= 0, with a relative error of at most 0.62 2^-24 down to -0.1, 1.3 2^-24
-// to -5 and 5.1 2^-24 to -87, and 0 below: n = the integer nearest to g / ln 2,
-// r = g - n ln 2, e^r = 1 + r + r^2 p(r) with p of degree 4 interpolating at
-// Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n added to the exponent.  The sum
-// g / ln 2 + 1.5 2^23 has n in its low bits.  ldexp adds it: NaN for a NaN whatever its
-// payload (which an integer sum would carry into the exponent), infinity for a gate above
-// 88.7, which has no business here.  12 instructions; the hardware
-// exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on average,
-// which a channel sums over all the tokens that it remembers (it would save 1 to 5 %).
+// e^g for g <= 0, with a relative error of at most 0.62 2^-24 down to -0.1 and 1.4 2^-24
+// to -87, and 0 below: n = the integer nearest to g / ln 2, r = g - n ln 2 with ln 2 in
+// two parts (rounded to one the error grows with n, to 5.1 2^-24), e^r = 1 + r + r^2 p(r)
+// with p of degree 4 interpolating at Chebyshev's nodes (2e-9 off on |r| <= ln 2 / 2), n
+// added to the exponent.  The sum g / ln 2 + 1.5 2^23 has n in its low bits.  ldexp adds
+// it: NaN for a NaN whatever its payload (which an integer sum would carry into the
+// exponent), infinity for a gate above 88.7, which has no business here.  13 instructions;
+// the hardware exponential takes the time of 5, but near 0 it is low by 0.12 2^-24 on
+// average, which a channel sums over all the tokens that it remembers (it would save 1
+// to 5 %).
 __device__ __forceinline__ float decay(float g) {
-    const float t = fmaf(g, 1.4426950408889634f, kRoundBias);
-    const float r = fmaf(t - kRoundBias, -0.6931471805599453f, g);
+    const float t = fmaf(g, 1.4426950408889634f, kRoundBias), n = t - kRoundBias;
+    const float r = fmaf(n, 1.9046543e-9f, fmaf(n, -0.6931471805599453f, g));
     float q = fmaf(r, 0.0013926184f, 0.008363179f);
     q = fmaf(r, q, 0.041666556f);
     q = fmaf(r, q, 0.16666576f);
