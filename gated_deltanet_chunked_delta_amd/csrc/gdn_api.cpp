@@ -474,7 +474,9 @@ int check_norm_ws(const gdn_norm_shape &s, const float *dweight, const void *wor
 
 // Sizes of a gated linear recurrence.
 constexpr int64_t kMaxScanTokens = INT_MAX - 1024;     // a tile behind the last token has a number of 32 bits too
-int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with_beta) {
+int scan_gate_f32(const gdn_scan_shape &s) { return s.gate_dtype == GDN_F32; }
+int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with_beta, bool backward = false,
+               bool held = false) {
     if (!shape) return GDN_ERR_NULL;
     const gdn_scan_shape &s = *shape;
     if (s.B < 0 || s.T < 0 || s.N < 0 || s.D <= 0 || s.D > (1 << 26)) return GDN_ERR_SHAPE;
@@ -485,7 +487,8 @@ int check_scan(const gdn_scan_shape *shape, const int32_t *cu_seqlens, bool with
     if (tokens > kMaxScanTokens || (s.N == 0 && tokens > 0)) return GDN_ERR_SHAPE;
     if (tokens > 0 && (s.x_stride < s.D || s.g_stride < s.D || (with_beta && s.beta_stride < s.D))) return GDN_ERR_SHAPE;
     if (s.x_stride > most || s.g_stride > most || (with_beta && s.beta_stride > most)) return GDN_ERR_SHAPE;
-    if (gdn::scan_grid(tokens, s.D, s.N) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (s.N > kMaxGrid || gdn::scan_grid(tokens, s.D, s.dtype, scan_gate_f32(s), with_beta, held, backward) > kMaxGrid)
+        return GDN_ERR_SHAPE;
     if (((uintptr_t)cu_seqlens & 3u) != 0) return GDN_ERR_ALIGN;
     return GDN_OK;
 }
@@ -505,7 +508,6 @@ gdn::ScanParams scan_params(const gdn_scan_shape &s, const void *x, const void *
     p.N = s.N;
     return p;
 }
-int scan_gate_f32(const gdn_scan_shape &s) { return s.gate_dtype == GDN_F32; }
 int check_scan_ws(const gdn_scan_shape &s, bool backward, const void *workspace, size_t workspace_bytes) {
     const size_t need = gdn::scan_workspace_bytes((int64_t)s.B * s.T, s.D, scan_gate_f32(s), backward);
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GDN_ERR_WORKSPACE;
@@ -954,6 +956,7 @@ int gdn_scan_steps(const void *x, const void *g, const void *beta, const gdn_ste
     int st = check_scan(shape, cu_seqlens, beta != nullptr);
     if (st != GDN_OK) return st;
     const gdn_scan_shape &s = *shape;
+    if (gdn::scan_steps_grid(s.N, s.D) > kMaxGrid) return GDN_ERR_SHAPE;
     if (!pool) return GDN_ERR_NULL;
     if (gdn::elem_bytes(pool->dtype) == 0) return GDN_ERR_DTYPE;
     if ((int64_t)s.B * s.T == 0) return GDN_OK;
@@ -975,7 +978,7 @@ int gdn_scan_bwd(const void *x, const void *g, const void *beta, const void *y, 
                  const gdn_held *y8, const void *dout, const float *dht, const float *initial_state,
                  const int32_t *cu_seqlens, void *dx, void *dg, void *dbeta, float *dinitial,
                  const gdn_scan_shape *shape, void *workspace, size_t workspace_bytes, void *stream) {
-    int st = check_scan(shape, cu_seqlens, beta != nullptr);
+    int st = check_scan(shape, cu_seqlens, beta != nullptr, true, y8 != nullptr);
     if (st != GDN_OK) return st;
     const gdn_scan_shape &s = *shape;
     const bool any = (int64_t)s.B * s.T > 0;

@@ -140,9 +140,10 @@ struct ScanParams {
 };
 // gate_f32: g, beta and their gradients are fp32 (else the element type).
 size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward);
-// 256-thread workgroups of the largest grid these sizes launch (host check against the
-// grid limit).
-int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N);
+// 256-thread workgroups that a pass over these sizes launches, and a few-token call at
+// most (host checks against the grid limit).
+int64_t scan_grid(int64_t T_tot, int D, int dtype, int gate_f32, bool beta, bool held, bool backward);
+int64_t scan_steps_grid(int64_t N, int D);
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
 hipError_t launch_scan_bwd(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);
 hipError_t launch_scan_steps(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof);

@@ -928,14 +928,11 @@ size_t scan_workspace_bytes(int64_t T_tot, int D, int gate_f32, bool backward) {
     });
     return most;
 }
-int64_t scan_grid(int64_t T_tot, int64_t D, int64_t N) {
-    int64_t most = N * steps_blocks((int)D);
-    for (int i = 0; i < 4; ++i)
-        each_tile((int)D, i & 1, i & 2, [&](const Tile &t) {
-            most = std::max(most, (int64_t)tiles_of(T_tot, t) * blocks_of((int)D, t) * (t.W * 64 / 256));
-        });
-    return most;
+int64_t scan_grid(int64_t T_tot, int D, int dtype, int gate_f32, bool beta, bool held, bool backward) {
+    const Tile t = tile_of(width_of(D), {backward, dtype != 0, gate_f32 != 0, beta, held});
+    return (int64_t)tiles_of(T_tot, t) * blocks_of(D, t) * (t.W * 64 / 256);
 }
+int64_t scan_steps_grid(int64_t N, int D) { return N * steps_blocks(D); }
 
 hipError_t launch_scan(const ScanParams &p, int dtype, int gate_f32, hipStream_t stream, Profiler *prof) {
     return launch_any(p, kForward, dtype, gate_f32, stream, prof);

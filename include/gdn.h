@@ -687,7 +687,8 @@ size_t gdn_scan_workspace_bytes(const gdn_scan_shape *shape, int backward);
  * workspace.  Tensors are aligned to their element.  Arithmetic is fp32, out
  * rounded once, and the result of a call does not depend on scheduling.  Returns
  * GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE (also tokens without a sequence, more than
- * 2^31 - 1025 of them, or too many for one launch: 2^23 - 1 tiles), GDN_ERR_DTYPE,
+ * 2^31 - 1025 of them, 2^24 sequences, or too many tokens and channels for one launch:
+ * 2^23 - 1 tiles, each of 32 tokens or more and up to 256 channels), GDN_ERR_DTYPE,
  * GDN_ERR_UNSUPPORTED (gate_dtype), GDN_ERR_ALIGN, GDN_ERR_WORKSPACE or
  * GDN_ERR_LAUNCH. */
 int gdn_scan_fwd(const void *x, const void *g, const void *beta, const float *initial_state,
@@ -705,7 +706,8 @@ int gdn_scan_fwd_pool(const void *x, const void *g, const void *beta, const gdn_
 /* The recurrence over a few tokens per sequence, states in a pool [pool_size, D],
  * fp32 or bf16 (aligned to their element): see gdn_step_pool.  A sequence's tokens
  * are taken in order by one wave.  No workspace; out must not overlap any input or
- * the pool. */
+ * the pool.  GDN_ERR_SHAPE also for 2^24 or more pairs of a sequence and a block of 256
+ * channels, and for what gdn_scan_fwd refuses. */
 int gdn_scan_steps(const void *x, const void *g, const void *beta, const gdn_step_pool *pool,
                    const int32_t *cu_seqlens, void *out, const gdn_scan_shape *shape, void *stream);
 

@@ -108,3 +108,18 @@ def test_the_decay_over_its_range(gate):
         assert over.max() <= 1.5, name
     low = torch.tensor([-87.5, -88.0, -1e3, -1e30, torch.finfo(gate).min, -float("inf")], device=DEV).to(gate).view(1, 1, -1)
     assert not gdn.gated_linear_recurrence(torch.zeros_like(low), low, initial_state=one[:, :6])[1].any()
+
+
+def test_a_million_sequences():
+    """2^20 sequences of one token of 4096 channels each: from zero, y and the final states are x, dx is dy + dht."""
+    gdn = _gdn()
+    N, D = 1 << 20, 4096
+    x = torch.randn(1, N, D, device=DEV, dtype=BF)
+    g = torch.full((1, 1, 1), -0.5, device=DEV, dtype=BF).expand(1, N, D).contiguous()
+    cu = torch.arange(N + 1, device=DEV, dtype=I32)
+    y, f = gdn.gated_linear_recurrence(x, g, cu_seqlens=cu)
+    assert torch.equal(y, x)
+    assert torch.equal(f, x[0].float())
+    del f
+    dx, dg, _, _ = gdn.gated_linear_recurrence_bwd(None, g, y, x, cu_seqlens=cu)
+    assert torch.equal(dx, x) and not dg.any()
