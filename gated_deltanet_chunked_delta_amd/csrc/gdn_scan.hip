@@ -13,6 +13,11 @@
 // nothing is read twice.  A pass over the data for the maps and another for the
 // outputs would read x and the gates twice.
 //
+// A product of decays may underflow to zero where no decay is zero: an infinite state
+// then becomes a NaN behind it, never a finite number.  To keep the infinity (products no
+// smaller than 2^-149 while no factor is zero) took 2 to 10 % of the passes (64 packed
+// prompts 650 -> 662 us, gradients of 64 x 4096 tokens of 32 channels 86 -> 94).
+//
 // Measured (GPU time): 131,072 tokens of 4096 channels with bf16 gates and no beta 650
 // us (4.9 TB/s of x, g and y; one thread a channel 106 ms); 64 packed prompts, 74,000
 // tokens of 4096, fp32 g and beta 636 us (5.7 TB/s; 2.66 ms); gradients of 16,384

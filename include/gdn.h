@@ -649,6 +649,10 @@ int gdn_add_norm_bwd(const void *dout, const void *dhidden, const void *hidden, 
  * strength (gdn_gating makes both, for any number of channels).  States are fp32.
  * g is not checked: a NaN makes the channel's states NaNs from there to the end of its
  * sequence, a gate above 0 grows them (e^g is infinite above 88.7).
+ * An infinity in x, beta or an initial state is never followed by a finite state in its
+ * sequence and channel; it may become a NaN where token by token it stayed an
+ * infinity, as the states go over many tokens by the product of their decays, which may
+ * be zero when none of them is.  The gradients have the same of dout and dht.
  *
  * Sizes.
  *   B, T, N       as in gdn_shape (with cu_seqlens B = 1)

@@ -111,7 +111,7 @@ def test_the_decay_over_its_range(gate):
 
 
 def test_a_million_sequences():
-    """2^20 sequences of one token of 4096 channels each: from zero, y and the final states are x, dx is dy + dht."""
+    """2^20 sequences of one token of 4096 channels each: from zero, y and the final states are x, and dx is dy."""
     gdn = _gdn()
     N, D = 1 << 20, 4096
     x = torch.randn(1, N, D, device=DEV, dtype=BF)
@@ -123,3 +123,48 @@ def test_a_million_sequences():
     del f
     dx, dg, _, _ = gdn.gated_linear_recurrence_bwd(None, g, y, x, cu_seqlens=cu)
     assert torch.equal(dx, x) and not dg.any()
+
+
+@pytest.mark.parametrize("D", [2, 40, 133])
+@pytest.mark.parametrize("dtype,gate", [(BF, F32), (BF, BF), (F32, F32)], ids=["bf16_fp32", "bf16", "fp32"])
+def test_no_state_is_finite_behind_an_infinity(dtype, gate, D):
+    """An infinite input, or one in the initial state, under decays whose product underflows within a strip of tokens, a
+    tile, or not at all: every later state of the channel's sequence is an infinity or a NaN, with small decays the
+    infinity; of gradients, every earlier one.  Other channels are the bits that they were."""
+    gdn = _gdn()
+    lens, at = (50, 5000, 30), 1700
+    cu, T = _cu(*lens), sum(lens)
+    x, _, b, dy = _inputs(D, T, D, dtype, gate)
+    gen = torch.Generator().manual_seed(5)
+    h0, dht = torch.randn(3, D, generator=gen).to(DEV), torch.randn(3, D, generator=gen).to(DEV)
+    inf = float("inf")
+    for rate in (1e-3, 0.5, 7.0, 60.0):
+        g = (-(torch.rand(1, T, D, generator=gen) + 0.5) * rate).to(gate).to(DEV)
+
+        def both(x, h0, dy, dht):
+            y, f = gdn.gated_linear_recurrence(x, g, b, initial_state=h0, cu_seqlens=cu)
+            return (y, f, *gdn.gated_linear_recurrence_bwd(x, g, y, dy, b, dht=dht, initial_state=h0, cu_seqlens=cu,
+                                                           output_dinitial=True))
+
+        clean = both(x, h0, dy, dht)
+        bad = [t.clone() for t in (x, h0, dy, dht)]
+        bad[0][0, at, 0] = -inf
+        bad[2][0, at, 0] = inf
+        bad[1][1, D - 1] = inf
+        bad[3][1, D - 1] = inf
+        got = both(*bad)
+        y, f, dx, _, _, dinitial = got
+        for t in (y[0, at:5050, 0], f[1, 0], y[0, 50:5050, D - 1], f[1, D - 1], dx[0, 50:at + 1, 0], dinitial[1, 0],
+                  dx[0, 50:5050, D - 1], dinitial[1, D - 1]):
+            assert not t.isfinite().any(), rate
+        if rate < 0.01:   # 5000 tokens are e^-10: no product is zero
+            assert (y[0, at:5050, 0] == -inf).all() and (y[0, 50:5050, D - 1] == inf).all()
+            assert (dx[0, 50:at + 1, 0] == inf).all() and dinitial[1, D - 1] == inf
+        for u, v in zip(got, clean):
+            same = torch.ones_like(u, dtype=torch.bool)
+            for ch in (0, D - 1):
+                if u.dim() == 2:
+                    same[1, ch] = False
+                else:
+                    same[0, 50:5050, ch] = False
+            assert torch.equal(u[same], v[same]), rate
