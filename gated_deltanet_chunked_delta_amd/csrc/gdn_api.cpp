@@ -572,7 +572,7 @@ int hold(void *values, const int32_t *value_index, const gdn_held *held, const i
     if (misaligned(s.dtype, values) || misaligned(GDN_F32, value_index, held_index)) return GDN_ERR_ALIGN;
     const gdn::QuantParams p{values, held_of(*held), value_index, held_index, s.n, s.D, s.stride, s.value_rows,
                              s.held_rows};
-    if (gdn::quant_grid(p, s.dtype, s.bits) > kMaxGrid) return GDN_ERR_SHAPE;
+    if (gdn::quant_grid(p, s.dtype, s.bits, back) > kMaxGrid) return GDN_ERR_SHAPE;
     const hipError_t err = with_profiler([&](gdn::Profiler *prof) {
         return gdn::launch_quant(p, s.dtype, s.bits, back, (hipStream_t)stream, prof);
     });

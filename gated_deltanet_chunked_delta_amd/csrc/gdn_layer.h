@@ -116,7 +116,7 @@ struct QuantParams {
     int value_rows, held_rows;
 };
 hipError_t launch_quant(const QuantParams &p, int dtype, int bits, bool back, hipStream_t stream, Profiler *prof);
-int64_t quant_grid(const QuantParams &p, int dtype, int bits);   // as for scan_grid
+int64_t quant_grid(const QuantParams &p, int dtype, int bits, bool back);   // as for scan_grid
 
 // The gated linear recurrence h_t = e^g_t h_(t-1) + beta_t x_t per channel.
 struct ScanParams {

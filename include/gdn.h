@@ -758,7 +758,7 @@ typedef struct gdn_held_shape {
  * alignment.  The tensors must not overlap.  Returns GDN_OK, GDN_ERR_NULL,
  * GDN_ERR_SHAPE (also n above value_rows or held_rows without that side's index, or
  * 2^31 rows, or too many for one launch: 2^24 - 1 workgroups of 8192 values of long
- * rows, of which rows of whole groups that follow each other are one, or of 2 to 64
+ * rows, of which rows of whole groups that follow each other are one, or of 2 to 256
  * rows of up to 1024 values), GDN_ERR_DTYPE,
  * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN or GDN_ERR_LAUNCH. */
 int gdn_hold(const void *values, const int32_t *value_index, const gdn_held *held, const int32_t *held_index,
