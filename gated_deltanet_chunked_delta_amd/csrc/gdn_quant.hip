@@ -203,7 +203,7 @@ Plan plan_of(const QuantParams &q, int elem, int bits, bool back) {
 template <typename E, int BITS, int U, bool STREAM, bool ROWS> void launch(const Plan &f, bool back, hipStream_t st) {
     if (back)
         dequant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
-    else if constexpr (!ROWS || !STREAM || (sizeof(E) == 2 && BITS == 8))
+    else if constexpr (!ROWS || U == 1 || STREAM == (sizeof(E) == 2 && BITS == 8))
         quant_kernel<E, BITS, U, STREAM, ROWS><<<(unsigned)f.grid, kThreads, 0, st>>>(f.p, f.split);
 }
 template <typename E, int BITS, bool ROWS> void launch_rows(const Plan &f, bool back, hipStream_t st) {
