@@ -99,7 +99,9 @@ __global__ void __launch_bounds__(threads_of(L)) norm_held_kernel(NormParams p, 
 // Workgroups of 512 threads: twice the waves of the norm's backward pass for as many
 // rows of partial sums, as there is more arithmetic for fewer bytes (524,288 rows of
 // 128: 117 us; with 256 threads, the next row's loads the only ones in flight, 174; with
-// 1024 119).
+// 1024 119).  Two of them a CU leave a lane 128 registers: bf16 rows above 128 and fp32 rows up
+// to 512 keep 12 to 40 bytes in scratch memory.  Without the limit a CU has one workgroup
+// (bf16 rows of 256 115 -> 174 us, 131,072 fp32 rows of 256 117 -> 114, 65,536 of 512 127 -> 114).
 constexpr int kBwdThreads = 512;
 template <typename E, int L, int NV, bool STREAM>
 __global__ void __launch_bounds__(kBwdThreads, NV == 1 ? 4 : 2) norm_held_bwd_kernel(NormParams p, Held x8, Held z8) {

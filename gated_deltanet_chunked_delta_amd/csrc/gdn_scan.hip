@@ -10,7 +10,8 @@
 // to a state is a map h -> A h + b, and maps compose: workgroups take tiles of tokens
 // and channels, keep them in registers, hand their maps on to the later ones (see
 // carry_in) and run through their tokens again with the state that comes in, so that
-// nothing is read twice.  A pass over the data for the maps and another for the
+// nothing is read twice: a single-pass scan with decoupled look-back (Merrill and
+// Garland 2016) of maps, composed in an order that the sizes fix.  A pass over the data for the maps and another for the
 // outputs would read x and the gates twice.
 //
 // A product of decays may underflow to zero where no decay is zero: an infinite state
@@ -18,15 +19,15 @@
 // smaller than 2^-149 while no factor is zero) took 2 to 10 % of the passes (64 packed
 // prompts 650 -> 662 us, gradients of 64 x 4096 tokens of 32 channels 86 -> 94).
 //
-// Measured (GPU time): 131,072 tokens of 4096 channels with bf16 gates and no beta 650
-// us (4.9 TB/s of x, g and y; one thread a channel 106 ms); 64 packed prompts, 74,000
-// tokens of 4096, fp32 g and beta 636 us (5.7 TB/s; 2.66 ms); gradients of 16,384
-// tokens of 4096 with fp32 gates 276 us (5.8 TB/s; 5.7 ms), of the packed prompts with
-// bf16 gates and x and y in 8 bits 893 us (4.8 TB/s; 3.3 ms).  Few tokens or channels
+// Measured (the call, workspace cleared): 131,072 tokens of 4096 channels with bf16 gates
+// and no beta 653 us (4.9 TB/s of x, g and y; one thread a channel 106 ms); 64 packed
+// prompts, 74,000 tokens of 4096, fp32 g and beta 648 us (5.6 TB/s; 2.66 ms); gradients of
+// 16,384 tokens of 4096 with fp32 gates 279 us (5.8 TB/s; 5.7 ms), of the packed prompts
+// with bf16 gates and x and y in 8 bits 905 us (4.7 TB/s; 3.3 ms).  Few tokens or channels
 // are bound by the latency of a tile, about 15 us: loads 3, decays and sums 3, maps
 // of other tiles 4, stores 2 (2042 tokens of 1001 channels in fp32 15 us, and 2 for
 // the workspace); long sequences of few channels by the states' way from block to
-// block (131,072 tokens of 256 channels 126 us, floor 84; 2^20 of 64 197, floor 84).
+// block (131,072 tokens of 256 channels 126 us, floor 68; 2^20 of 64 196, floor 68).
 #include <algorithm>
 #include <type_traits>
 
@@ -824,6 +825,15 @@ enum Pass { kForward, kBackward, kSteps };
 //     tensors two by 8 374, by 10 413; held four by 4 276, two by 10 425
 //   backward, bf16 gates: two channels by 14 tokens 732, four by 8 758; held four by 6
 //     896, by 5 962, by 7 959; without beta four by 10 265, by 8 274, two by 16 270
+//   up to 64 channels, bf16 gates, 10 tokens forward and 5 backward against 8 and 4: 2^20
+//     tokens of 64 channels 195 and 202; 16 sequences of 16,384 tokens of 32 channels with beta
+//     65.5 and 65.4, without 54.1 and 53.2, gradients 92 and 92, without beta 74 and 81, from 8
+//     bits 94 and 91.  fp32 gates, 8 and 4 against 6 and 3: 2^20 of 8 204 and 253, gradients
+//     375 and 456, the 16 sequences 74 and 62, gradients 126 and 117: the fewer tiles count where
+//     they follow one another.
+// Some tiles keep a few values in scratch memory all the same: with fp32 gates and beta above 64
+// channels 8 bytes a lane, up to 64 channels 56 to 136 forward and 20 to 148 backward (not the
+// gradients without beta of bf16 tensors).
 struct Tile {
     int VC, W, S, R;
     constexpr int tokens() const { return W * R * S; }
