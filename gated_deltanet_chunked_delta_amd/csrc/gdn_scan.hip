@@ -27,7 +27,7 @@
 // are bound by the latency of a tile, about 15 us: loads 3, decays and sums 3, maps
 // of other tiles 4, stores 2 (2042 tokens of 1001 channels in fp32 15 us, and 2 for
 // the workspace); long sequences of few channels by the states' way from block to
-// block (131,072 tokens of 256 channels 126 us, floor 68; 2^20 of 64 196, floor 68).
+// block (131,072 tokens of 256 channels 126 us, floor 68; 2^20 of 64 177, floor 68).
 #include <algorithm>
 #include <type_traits>
 
@@ -157,6 +157,17 @@ template <typename E> __device__ __forceinline__ const E *at(const void *base, i
 }
 template <typename E> __device__ __forceinline__ E *at(void *base, int64_t row, int64_t stride, uint32_t c) {
     return (E *)((char *)((E *)base + row * stride) + c * (uint32_t)sizeof(E));
+}
+// Token s of a strip that begins at token tw.  Where a wave has several strips their rows
+// differ from lane to lane, and an address of its own for each token would take more
+// registers than there are (gradients of 16 sequences of 16,384 tokens of 32 channels in
+// fp32 152 us, with one address a strip 131).
+template <int R, typename E>
+__device__ __forceinline__ const E *token(const void *base, int tw, int s, int64_t stride, uint32_t c) {
+    return R == 1 ? at<E>(base, tw + s, stride, c) : at<E>(base, tw, stride, c) + s * stride;
+}
+template <int R, typename E> __device__ __forceinline__ E *token(void *base, int tw, int s, int64_t stride, uint32_t c) {
+    return R == 1 ? at<E>(base, tw + s, stride, c) : at<E>(base, tw, stride, c) + s * stride;
 }
 template <int VC> __device__ __forceinline__ Lane lane_of(int D, int ncb, int cb, int lane) {
     const int nv = (D + VC - 1) / VC, units = (nv + 15) / 16, each = units / ncb, more = units % ncb;
@@ -461,17 +472,25 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
     typename RE::T xr[S];
     typename RG::T gr[S], br[S];
     float a[S][VC], u[RAW ? 1 : S][VC];
-    // every lane loads, those without channels another's and those without tokens the
-    // last token, so that the loads are issued in one run
+    // With a strip a wave every lane loads, those without channels another's and those
+    // without tokens the last token, so that the loads are issued in one run; with several
+    // only those that have both.
+    const int last = R == 1 ? t_end - 1 - tw : S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        const int row = min(tw + s, t_end - 1);
-        xr[s] = RE::template load<STREAM>(at<E>(p.x, row, p.x_stride, ln.c));
-        gr[s] = RG::template load<STREAM>(at<G>(p.g, row, p.g_stride, ln.c));
-        if (BETA) br[s] = RG::template load<STREAM>(at<G>(p.beta, row, p.beta_stride, ln.c));
+        if constexpr (R > 1) {
+            xr[s] = RE::zero();
+            gr[s] = RG::zero();
+            if (BETA) br[s] = RG::zero();
+            if (s >= nv || !ln.live) continue;
+        }
+        const int t = min(s, last);
+        xr[s] = RE::template load<STREAM>(token<R, E>(p.x, tw, t, p.x_stride, ln.c));
+        gr[s] = RG::template load<STREAM>(token<R, G>(p.g, tw, t, p.g_stride, ln.c));
+        if (BETA) br[s] = RG::template load<STREAM>(token<R, G>(p.beta, tw, t, p.beta_stride, ln.c));
     }
     find_sequences<TT, NT>(q, p, t0, t_end);
-    if (nv < S)                                        // no token: a = 1, u = 0, the state stays
+    if (R == 1 && nv < S)                              // no token: a = 1, u = 0, the state stays
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (s >= nv) {
@@ -561,7 +580,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
             h[e] = fmaf(a[s][e], h[e], taken(s, e));
             RE::set(o, e, h[e]);
         }
-        if (s < stored) RE::template store<STREAM>(at<E>(p.y, tw + s, p.D, ln.c), o);
+        if (s < stored) RE::template store<STREAM>(token<R, E>(p.y, tw, s, p.D, ln.c), o);
         if ((ends >> s & 1) && p.final_state && ln.live) {
             int64_t to = (int64_t)seq * p.D + ln.c;
             bool kept = true;
@@ -579,6 +598,7 @@ __global__ void __launch_bounds__(W * 64, 4) scan_kernel(ScanParams p, int ncb, 
 // those of a lane lie in two groups where vectors overlap (two, see lane_of).
 template <typename E, int VC, bool HELD, bool STREAM> struct Saved {
     typename Vector<E, VC>::T r;
+    __device__ __forceinline__ void clear() { r = Vector<E, VC>::zero(); }
     __device__ __forceinline__ void load(const void *v, const Held &, int64_t row, int64_t stride, int, uint32_t c, bool) {
         r = Vector<E, VC>::template load<STREAM>(at<E>(v, row, stride, c));
     }
@@ -586,6 +606,7 @@ template <typename E, int VC, bool HELD, bool STREAM> struct Saved {
 };
 template <typename E, int VC, bool STREAM> struct Saved<E, VC, true, STREAM> {
     uint32_t codes, scales;                            // scales: of the first value's group low, of the last one's high
+    __device__ __forceinline__ void clear() { codes = scales = 0; }
     __device__ __forceinline__ void load(const void *, const Held &h, int64_t row, int64_t, int D, uint32_t c, bool two) {
         const uint8_t *src = at<uint8_t>(h.codes, row, D, c);
         const int groups = (D + kGroup - 1) / kGroup;
@@ -631,14 +652,20 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     typename RE::T dr[S];
     typename RG::T gr[S], br[S];
     float a[RAW ? 1 : S][VC];
+    const int ahead = R == 1 ? t_end - 1 - tw : S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {                      // see scan_kernel
-        const int row = min(tw + s, t_end - 1);
-        dr[s] = RE::template load<STREAM>(at<E>(p.dy, row, p.D, ln.c));
-        gr[s] = RG::template load<STREAM>(at<G>(p.g, row, p.g_stride, ln.c));
+        if constexpr (R > 1) {
+            dr[s] = RE::zero();
+            gr[s] = RG::zero();
+            if (s >= nv || !ln.live) continue;
+        }
+        const int t = min(s, ahead);
+        dr[s] = RE::template load<STREAM>(token<R, E>(p.dy, tw, t, p.D, ln.c));
+        gr[s] = RG::template load<STREAM>(token<R, G>(p.g, tw, t, p.g_stride, ln.c));
     }
     find_sequences<TT, NT>(q, p, t0, t_end);
-    if (nv < S)
+    if (R == 1 && nv < S)
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (s >= nv) {
@@ -660,11 +687,19 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
     SV yr[S], xr[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        const int row = min(tw + s, t_end - 1);
-        yr[s].load(p.y, p.y8, max(row - 1, 0), p.D, p.D, ln.c, two);
+        if constexpr (R > 1) {
+            yr[s].clear();
+            if (BETA) {
+                xr[s].clear();
+                br[s] = RG::zero();
+            }
+            if (s >= nv || !ln.live) continue;
+        }
+        const int t = min(s, ahead);
+        yr[s].load(p.y, p.y8, max(tw + t - 1, 0), p.D, p.D, ln.c, two);
         if (BETA) {
-            xr[s].load(p.x, p.x8, row, p.x_stride, p.D, ln.c, two);
-            br[s] = RG::template load<STREAM>(at<G>(p.beta, row, p.beta_stride, ln.c));
+            xr[s].load(p.x, p.x8, tw + t, p.x_stride, p.D, ln.c, two);
+            br[s] = RG::template load<STREAM>(token<R, G>(p.beta, tw, t, p.beta_stride, ln.c));
         }
     }
     const bool is = lane < nv;
@@ -737,9 +772,9 @@ __global__ void __launch_bounds__(W * 64, 4) scan_bwd_kernel(ScanParams p, int n
             }
         }
         if (s < stored) {
-            RE::template store<STREAM>(at<E>(p.dx, tw + s, p.D, ln.c), ox);
-            RG::template store<STREAM>(at<G>(p.dg, tw + s, p.D, ln.c), og);
-            if (BETA) RG::template store<STREAM>(at<G>(p.dbeta, tw + s, p.D, ln.c), ob);
+            RE::template store<STREAM>(token<R, E>(p.dx, tw, s, p.D, ln.c), ox);
+            RG::template store<STREAM>(token<R, G>(p.dg, tw, s, p.D, ln.c), og);
+            if (BETA) RG::template store<STREAM>(token<R, G>(p.dbeta, tw, s, p.D, ln.c), ob);
         }
         if (first && p.dinitial && ln.live) store_states<VC>(p.dinitial, (int64_t)n * p.D + ln.c, 0, c);
     }
@@ -839,7 +874,7 @@ struct Tile {
     constexpr int tokens() const { return W * R * S; }
 };
 // By the number of channels: one a lane below 4, four strips a wave up to 64 (2^20
-// tokens of 8 channels with one strip a wave: 715 against 204 us, of 64 274 against 197).
+// tokens of 8 channels with one strip a wave: 715 against 193 us, of 64 274 against 177).
 enum Width { kOne, kNarrow, kWide };
 Width width_of(int D) { return D < 4 ? kOne : D <= 64 ? kNarrow : kWide; }
 // What a call's tensors are, as far as its tiles go by it.
