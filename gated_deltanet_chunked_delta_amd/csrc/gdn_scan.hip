@@ -860,15 +860,15 @@ enum Pass { kForward, kBackward, kSteps };
 //     tensors two by 8 374, by 10 413; held four by 4 276, two by 10 425
 //   backward, bf16 gates: two channels by 14 tokens 732, four by 8 758; held four by 6
 //     896, by 5 962, by 7 959; without beta four by 10 265, by 8 274, two by 16 270
-//   up to 64 channels, bf16 gates, 10 tokens forward and 5 backward against 8 and 4: 2^20
-//     tokens of 64 channels 195 and 202; 16 sequences of 16,384 tokens of 32 channels with beta
-//     65.5 and 65.4, without 54.1 and 53.2, gradients 92 and 92, without beta 74 and 81, from 8
-//     bits 94 and 91.  fp32 gates, 8 and 4 against 6 and 3: 2^20 of 8 204 and 253, gradients
-//     375 and 456, the 16 sequences 74 and 62, gradients 126 and 117: the fewer tiles count where
-//     they follow one another.
+//   up to 64 channels, 2^20 tokens of 64 or 8 channels, and 16 sequences of 16,384 of 32:
+//     forward, bf16 gates, 10 tokens 179, 175 and 57, 8 203, 186 and 61; fp32 gates 8 tokens (8
+//     channels) 193 and 66, 7 221 and 62
+//     backward, bf16 gates with beta 5 tokens 191 (64 channels) and 89, 8 195 and 97, from 8 bits 92
+//     and 101; without beta 8 tokens 242, 193 and 63, 5 314, 286 and 73 (8 sequences of 2048 of 64
+//     channels 22.5 and 20.9); below 4 channels 8 tokens 128 and without beta 122, 5 166 and 167
 // Some tiles keep a few values in scratch memory all the same: with fp32 gates and beta above 64
-// channels 8 bytes a lane, up to 64 channels 56 to 136 forward and 20 to 148 backward (not the
-// gradients without beta of bf16 tensors).
+// channels 8 bytes a lane, from 4 to 64 channels 20 to 100 forward and, but without beta and with
+// fp32 gates, 8 to 100 backward.
 struct Tile {
     int VC, W, S, R;
     constexpr int tokens() const { return W * R * S; }
@@ -882,7 +882,8 @@ struct Kind {
     bool backward, f32, gate_f32, beta, held;
 };
 constexpr Tile tile_of(Width width, Kind k) {
-    if (width != kWide) return {width == kOne ? 1 : 4, 8, k.backward ? (k.gate_f32 ? 4 : 5) : k.gate_f32 ? 8 : 10, 4};
+    if (width == kOne) return {1, 8, k.backward ? (k.gate_f32 ? 4 : 8) : k.gate_f32 ? 8 : 10, 4};
+    if (width == kNarrow) return {4, 8, k.backward ? (k.gate_f32 ? 4 : k.beta ? 5 : 8) : k.gate_f32 ? 8 : 10, 4};
     if (!k.backward)
         return k.gate_f32 ? (k.beta ? Tile{4, 8, 8, 1} : Tile{2, 8, 20, 1}) : Tile{2, 8, k.beta ? 20 : 28, 1};
     if (k.gate_f32) return k.held ? Tile{4, 8, 4, 1} : Tile{2, 8, k.f32 ? 8 : 10, 1};
